@@ -47,7 +47,7 @@
 extern "C" {
 #endif
 
-#define QSA_ABI_VERSION 2
+#define QSA_ABI_VERSION 3
 
 typedef enum {
   QSA_OK = 0,
@@ -65,6 +65,8 @@ typedef enum {
 #define QSA_STATUS_TIMEOUT 2  /* a pipeline wait inside the kernel exceeded its
                                  2 s bound; the kernel stopped early and its
                                  outputs are not valid */
+#define QSA_STATUS_BAD_POSITION 4 /* some position was outside the rotation table
+                                     (appends only; nothing of that token was written) */
 
 
 typedef struct {
@@ -459,6 +461,104 @@ qsa_status_t qsa_topk_select(const qsa_indexer_shape_t* shape,
                              int32_t append_tail, int32_t* lists,
                              int64_t list_stride_tok, int32_t* n_valid,
                              int32_t copies, int32_t* status, void* stream);
+
+/*
+ * KV-cache append with position rotation.  The attention entry points above
+ * read a cache whose keys are already rotated; these calls write it.  For
+ * every token t at position p = positions[t] and each pair (a, b) of the R =
+ * rotary_dim rotary dims of every Q and K head, with i the pair's number and
+ * cos_sin[p] = [cos_0 .. cos_{R/2-1}, sin_0 .. sin_{R/2-1}],
+ *
+ *   y_a = x_a cos_i - x_b sin_i,    y_b = x_b cos_i + x_a sin_i;
+ *
+ * dims R..255 and V pass through.  The K and V rows then go to cache row
+ * slots[t] (the physical slot ids that the attention's lists name; with a
+ * paged cache, page * page_size + offset) and the rotated Q to q_out.
+ */
+typedef struct {
+  int64_t num_tokens;     /* T >= 0 */
+  int32_t num_q_heads;    /* Hq >= 0; 0: no query, q and q_out are ignored */
+  int32_t num_kv_heads;   /* Hkv >= 1 */
+  int32_t head_dim;       /* must be 256 */
+  int32_t rotary_dim;     /* R: 0 .. 256, a multiple of 16; 0: no rotation,
+                             cos_sin and positions are ignored */
+  int32_t interleaved;    /* 0: pair i is dims (i, i + R/2); 1: (2i, 2i + 1) */
+  int32_t reserved;       /* 0 */
+  int64_t num_slots;      /* S: rows of the cache */
+  int64_t num_positions;  /* P: rows of cos_sin */
+  /* strides in elements; rows start on 16-byte boundaries */
+  int64_t q_stride_tok, q_stride_head;     /* q     [T, Hq, 256] BF16 */
+  int64_t qo_stride_tok, qo_stride_head;   /* q_out [T, Hq, 256] BF16 */
+  int64_t k_stride_tok, k_stride_head;     /* k     [T, Hkv, 256] BF16 */
+  int64_t v_stride_tok, v_stride_head;     /* v     [T, Hkv, 256] BF16 */
+  int64_t table_stride;                    /* cos_sin [P, >= R] FP32, rows a
+                                              multiple of 4 */
+  int64_t kv_stride_slot, kv_stride_head;  /* both caches (4-bit: the codes, in
+                                              bytes) */
+  int64_t bscale_stride_slot, bscale_stride_head; /* 4-bit: the block scales, in
+                                              bytes, multiples of 16 */
+} qsa_append_shape_t;
+
+/*
+ * Append to a BF16 cache.  q_out may be q itself (with q's strides; then
+ * only the rotary dims move) or a buffer that does not overlap it; no other
+ * output may overlap an input.  positions, slots: int32 device [T].
+ *  - slots[t] < 0: a padded row; its Q is rotated, nothing is cached.
+ *  - slots[t] >= S: nothing is cached and status bit 0 is set.
+ *  - positions[t] outside [0, P) (R > 0): nothing of the token is written,
+ *    q_out included, and status bit 2 is set.
+ *  - slots of one call must differ: what a row named twice ends as is
+ *    unspecified (its bytes come from the tokens that named it).
+ * Cache rows that no token names are not touched.  Rotation in FP32, one
+ * rounding to BF16.  QSA_ERR_SHAPE when the strides make rows that are
+ * written overlap.  One launch; no allocation, no sync, graph-capturable.
+ */
+qsa_status_t qsa_kv_append(const qsa_append_shape_t* shape, const void* q,
+                           void* q_out, const void* k, const void* v,
+                           const float* cos_sin, const int32_t* positions,
+                           const int32_t* slots, void* k_cache, void* v_cache,
+                           int32_t* status, void* stream);
+
+/*
+ * Append to an FP8 E4M3 cache: byte = E4M3 value nearest to y / k_scale (V:
+ * v_scale), ties to even, saturating at +-448; NaN stays NaN.  k_seen and
+ * v_seen (BF16 device [T, Hkv, 256] contiguous, or NULL) receive the values
+ * as cached, stored value * scale, of every token whose position is valid
+ * (padded ones included).  Scales must lie in [2^-100, 2^100]
+ * (QSA_ERR_UNSUPPORTED); cache strides are multiples of 16.  Otherwise as
+ * qsa_kv_append.
+ */
+qsa_status_t qsa_kv_append_fp8(const qsa_append_shape_t* shape, const void* q,
+                               void* q_out, const void* k, const void* v,
+                               const float* cos_sin, const int32_t* positions,
+                               const int32_t* slots, float k_scale,
+                               float v_scale, void* k_cache, void* v_cache,
+                               void* k_seen, void* v_seen, int32_t* status,
+                               void* stream);
+
+/*
+ * Append to a 4-bit cache.  A row holds 128 bytes of E2M1 codes (element 2i
+ * in the low half of byte i; magnitudes 0 .5 1 1.5 2 3 4 6, bit 3 the sign)
+ * and 16 E4M3 block scales, one per 16 dims; an element is code * block scale
+ * * k_scale (v_scale).  K codes, K block scales, V codes and V block scales
+ * have a pointer each; K and V share strides.  One buffer with rows of 288
+ * bytes [K codes, V codes, K block scales, V block scales] keeps what one key
+ * needs in nine 32-byte sectors.  Per block of 16 dims
+ *   e    = E4M3 value nearest to fl32(max |y|) * fl32(1 / fl32(6 k_scale)),
+ *          saturating at 448, and
+ *   code = E2M1 value nearest to y / (e k_scale), ties to the even code,
+ *          saturating at 6 (0 when e is 0),
+ * with y rotated in FP64 and the codes decided exactly.  A block with a NaN
+ * gets a NaN scale.  k_seen / v_seen: the values as cached, rounded to BF16.
+ * Otherwise as qsa_kv_append_fp8.
+ */
+qsa_status_t qsa_kv_append_fp4(const qsa_append_shape_t* shape, const void* q,
+                               void* q_out, const void* k, const void* v,
+                               const float* cos_sin, const int32_t* positions,
+                               const int32_t* slots, float k_scale,
+                               float v_scale, void* k_codes, void* k_bscale,
+                               void* v_codes, void* v_bscale, void* k_seen,
+                               void* v_seen, int32_t* status, void* stream);
 
 /* Static description of a status code. */
 const char* qsa_status_string(qsa_status_t status);

@@ -12,7 +12,8 @@ _API = ("sparse_prefill_fwd", "sparse_prefill_debug_gather", "sparse_prefill_fwd
         "sparse_decode_fwd", "sparse_decode_fwd_noalloc", "sparse_decode_fp8_fwd",
         "decode_workspace_bytes", "decode_num_splits",
         "indexer_scores", "topk_select", "indexer_select",
-        "status_string", "abi_version", "QSAError", "STATUS_OOB_SLOT", "STATUS_TIMEOUT")
+        "kv_append", "kv_append_fp8", "kv_append_fp4", "Fp4Cache", "fp4_cache", "rope_table",
+        "status_string", "abi_version", "QSAError", "STATUS_OOB_SLOT", "STATUS_TIMEOUT", "STATUS_BAD_POSITION")
 
 
 def __getattr__(name):

@@ -26,6 +26,7 @@ QSA_OK, QSA_ERR_NULL, QSA_ERR_SHAPE, QSA_ERR_UNSUPPORTED, QSA_ERR_ALIGN, QSA_ERR
 NOALLOC_SCRATCH_BYTES = 16 << 20
 STATUS_OOB_SLOT = 1
 STATUS_TIMEOUT = 2
+STATUS_BAD_POSITION = 4
 KERNEL_AUTO, KERNEL_TCGEN05, KERNEL_WARP_MMA = 0, 1, 2
 KERNELS = {"auto": KERNEL_AUTO, "tcgen05": KERNEL_TCGEN05, "warp_mma": KERNEL_WARP_MMA}
 HEAD_DIM = 256
@@ -36,7 +37,7 @@ EXPORTS = ("qsa_sparse_prefill_fwd", "qsa_sparse_prefill_fwd_with", "qsa_sparse_
            "qsa_sparse_prefill_fwd_host", "qsa_sparse_decode_fwd", "qsa_sparse_decode_workspace_bytes",
            "qsa_sparse_decode_num_splits", "qsa_sparse_decode_fwd_noalloc",
            "qsa_sparse_prefill_fp8_fwd", "qsa_sparse_decode_fp8_fwd", "qsa_indexer_scores",
-           "qsa_indexer_fold_heads", "qsa_topk_select", "qsa_status_string", "qsa_abi_version")
+           "qsa_indexer_fold_heads", "qsa_topk_select", "qsa_kv_append", "qsa_kv_append_fp8", "qsa_kv_append_fp4", "qsa_status_string", "qsa_abi_version")
 
 
 class Shape(ctypes.Structure):
@@ -71,6 +72,33 @@ class IndexerShape(ctypes.Structure):
         ("q_stride_head", ctypes.c_int64),
         ("k_stride_block", ctypes.c_int64),
         ("score_stride_tok", ctypes.c_int64),
+    ]
+
+
+class AppendShape(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", ctypes.c_int64),
+        ("num_q_heads", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("num_slots", ctypes.c_int64),
+        ("num_positions", ctypes.c_int64),
+        ("q_stride_tok", ctypes.c_int64),
+        ("q_stride_head", ctypes.c_int64),
+        ("qo_stride_tok", ctypes.c_int64),
+        ("qo_stride_head", ctypes.c_int64),
+        ("k_stride_tok", ctypes.c_int64),
+        ("k_stride_head", ctypes.c_int64),
+        ("v_stride_tok", ctypes.c_int64),
+        ("v_stride_head", ctypes.c_int64),
+        ("table_stride", ctypes.c_int64),
+        ("kv_stride_slot", ctypes.c_int64),
+        ("kv_stride_head", ctypes.c_int64),
+        ("bscale_stride_slot", ctypes.c_int64),
+        ("bscale_stride_head", ctypes.c_int64),
     ]
 
 
@@ -121,6 +149,9 @@ _lib.qsa_indexer_scores.argtypes = [ctypes.POINTER(IndexerShape), _vp, _vp, _vp,
 _lib.qsa_indexer_fold_heads.argtypes = [ctypes.POINTER(IndexerShape), _vp, _vp, _vp]
 _lib.qsa_topk_select.argtypes = [ctypes.POINTER(IndexerShape), _vp, _vp, _vp, ctypes.c_int64, ctypes.c_int32,
                                  _vp, ctypes.c_int64, _vp, ctypes.c_int32, _vp, _vp]
+_lib.qsa_kv_append.argtypes = [ctypes.POINTER(AppendShape)] + [_vp] * 11
+_lib.qsa_kv_append_fp8.argtypes = ([ctypes.POINTER(AppendShape)] + [_vp] * 7 + [ctypes.c_float] * 2 + [_vp] * 6)
+_lib.qsa_kv_append_fp4.argtypes = ([ctypes.POINTER(AppendShape)] + [_vp] * 7 + [ctypes.c_float] * 2 + [_vp] * 8)
 _lib.qsa_status_string.restype = ctypes.c_char_p
 _lib.qsa_status_string.argtypes = [ctypes.c_int]
 _lib.qsa_abi_version.restype = ctypes.c_int32
@@ -159,6 +190,18 @@ def _need(x: torch.Tensor, name: str, dtype, device=None, host=False):
             raise ValueError(f"{name} must be a host tensor")
     elif x.device.type != "cuda" or (device is not None and x.device != device):
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
+
+
+def _device_call(dev, stream, fn, *args):
+    """fn(*args, stream) with `dev` current: the library launches on the
+    current device, and a tensor's device need not be that one.  `stream`
+    None is dev's current stream."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev).cuda_stream
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        return _raise(fn(*args, stream))
+    with torch.cuda.device(dev):
+        return _raise(fn(*args, stream))
 
 
 def make_shape(q, k_cache, topk_idx, out, lse=None) -> Shape:
@@ -660,3 +703,166 @@ def indexer_select(q_idx, k_idx, positions, seq_start, budget: int, block_size: 
     lists, nv = topk_select(scores, positions, seq_start, k_idx.shape[0], budget, block_size, append_tail,
                             copies=copies, stream=stream)
     return lists, nv, scores
+
+
+# ------------------------------------------------------------------ cache append, 4-bit cache
+
+FP4_ROW_BYTES = 288     # K codes 128, V codes 128, K block scales 16, V block scales 16
+
+
+class Fp4Cache:
+    """A 4-bit KV cache over one uint8 buffer [S, Hkv, 288] (rows may be
+    strided): per slot and KV head 128 bytes of K codes, 128 of V codes, 16 K
+    and 16 V block scales.  `fp4_cache` allocates one."""
+
+    __slots__ = ("buffer",)
+
+    def __init__(self, buffer: torch.Tensor):
+        if buffer.dtype != torch.uint8:
+            raise TypeError(f"an Fp4Cache buffer must be torch.uint8, got {buffer.dtype}")
+        if buffer.dim() != 3 or buffer.shape[2] != FP4_ROW_BYTES or buffer.stride(2) != 1:
+            raise ValueError(f"an Fp4Cache buffer must be [S, Hkv, {FP4_ROW_BYTES}] with contiguous rows")
+        self.buffer = buffer
+
+    @property
+    def k_codes(self):
+        return self.buffer[..., :128]
+
+    @property
+    def v_codes(self):
+        return self.buffer[..., 128:256]
+
+    @property
+    def k_bscale(self):
+        return self.buffer[..., 256:272].view(torch.float8_e4m3fn)
+
+    @property
+    def v_bscale(self):
+        return self.buffer[..., 272:].view(torch.float8_e4m3fn)
+
+
+def fp4_cache(num_slots: int, num_kv_heads: int, device="cuda") -> Fp4Cache:
+    """A zeroed 4-bit KV cache of `num_slots` rows."""
+    return Fp4Cache(torch.zeros((num_slots, num_kv_heads, FP4_ROW_BYTES), dtype=torch.uint8, device=device))
+
+
+def rope_table(num_positions: int, rotary_dim: int, base: float = 10000.0, device="cuda"):
+    """cos_sin for the appends: [num_positions, rotary_dim] FP32, row p =
+    [cos(p f_i), sin(p f_i)] with f_i = base^(-2 i / rotary_dim), the angles
+    in FP64 (an FP32 angle of a far position is off by whole hundredths)."""
+    f = base ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64, device=device) / rotary_dim)
+    a = torch.arange(num_positions, dtype=torch.float64, device=device)[:, None] * f
+    return torch.cat((a.cos(), a.sin()), 1).float()
+
+
+def _append_args(k, v, positions, slots, cos_sin, caches, cache_dtype, q, q_out, interleaved, status):
+    """Checks and the shape descriptor of an append; returns (shape, q_out)."""
+    dev = k.device
+    _need(k, "k", torch.bfloat16, dev)
+    _need(v, "v", torch.bfloat16, dev)
+    if k.dim() != 3 or v.shape != k.shape:
+        raise ValueError("k and v must be [T, Hkv, 256]")
+    T, Hkv, Dh = k.shape
+    for name, c in caches:
+        _need(c, name, cache_dtype, dev)
+        if c.dim() != 3 or c.shape[1] != Hkv:
+            raise ValueError(f"{name} must be [S, Hkv, ...] with {Hkv} KV heads")
+        if c.stride(2) != 1:
+            raise ValueError("innermost dimensions must be contiguous")
+    cache = caches[0][1]
+    if k.stride(2) != 1 or v.stride(2) != 1:
+        raise ValueError("innermost dimensions must be contiguous")
+    _need_tok(slots, "slots", T, dev)
+    R = P = ts = 0
+    if cos_sin is not None:
+        _need(cos_sin, "cos_sin", torch.float32, dev)
+        if cos_sin.dim() != 2 or (cos_sin.shape[1] > 1 and cos_sin.stride(1) != 1):
+            raise ValueError("cos_sin must be [P, R] with contiguous rows")
+        P, R = cos_sin.shape
+        ts = cos_sin.stride(0) if P > 1 else R
+        if R > 0:
+            _need_tok(positions, "positions", T, dev)
+    Hq = 0
+    qs = qos = (0, 0)
+    if q is not None:
+        _need(q, "q", torch.bfloat16, dev)
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != Dh or q.stride(2) != 1:
+            raise ValueError("q must be [T, Hq, 256] with contiguous rows")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        _need(q_out, "q_out", torch.bfloat16, dev)
+        if q_out.shape != q.shape or q_out.stride(2) != 1:
+            raise ValueError("q_out must have q's shape and contiguous rows")
+        Hq = q.shape[1]
+        qs, qos = (q.stride(0), q.stride(1)), (q_out.stride(0), q_out.stride(1))
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    if status is not None:
+        _need(status, "status", torch.int32, dev)
+    shape = AppendShape(T, Hq, Hkv, Dh, R, 1 if interleaved else 0, 0, cache.shape[0], P, *qs, *qos,
+                        k.stride(0), k.stride(1), v.stride(0), v.stride(1), ts, cache.stride(0), cache.stride(1), 0, 0)
+    return shape, q_out
+
+
+def _seen_args(k, k_seen, v_seen, want_seen):
+    if want_seen:
+        k_seen = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device) if k_seen is None else k_seen
+        v_seen = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device) if v_seen is None else v_seen
+    for name, x in (("k_seen", k_seen), ("v_seen", v_seen)):
+        if x is not None:
+            _need(x, name, torch.bfloat16, k.device)
+            if x.shape != k.shape or not x.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous [T, Hkv, 256] tensor")
+    return k_seen, v_seen
+
+
+def kv_append(k, v, positions, slots, cos_sin, k_cache, v_cache, q=None, q_out=None, interleaved: bool = False,
+              status=None, stream=None):
+    """Rotates the new keys k [T, Hkv, 256] (and, when given, the query q
+    [T, Hq, 256]) by cos_sin [P, R] at `positions` and writes k and v to the
+    rows `slots` (int32 [T]; negative: padding, not cached) of BF16 caches
+    [S, Hkv, 256].  Returns the rotated query (q_out; q itself is allowed)."""
+    _check_kv(k_cache, v_cache)
+    shape, q_out = _append_args(k, v, positions, slots, cos_sin, (("k_cache", k_cache), ("v_cache", v_cache)),
+                                torch.bfloat16, q, q_out, interleaved, status)
+    if k_cache.shape[2] != k.shape[2]:
+        raise ValueError("k_cache must be [S, Hkv, 256]")
+    _device_call(k.device, stream, _lib.qsa_kv_append, ctypes.byref(shape), _ptr(q), _ptr(q_out), _ptr(k), _ptr(v),
+                 _ptr(cos_sin), _ptr(positions), _ptr(slots), _ptr(k_cache), _ptr(v_cache), _ptr(status))
+    return q_out
+
+
+def kv_append_fp8(k, v, positions, slots, cos_sin, k_cache, v_cache, k_scale: float = 1.0, v_scale: float = 1.0,
+                  q=None, q_out=None, interleaved: bool = False, k_seen=None, v_seen=None, want_seen: bool = False,
+                  status=None, stream=None):
+    """kv_append to FP8 E4M3 caches (torch.float8_e4m3fn), stored value = y /
+    k_scale (v_scale).  Returns (q_out, k_seen, v_seen): the last two, the
+    values as cached in BF16, are None unless given or asked for."""
+    _check_kv(k_cache, v_cache)
+    shape, q_out = _append_args(k, v, positions, slots, cos_sin, (("k_cache", k_cache), ("v_cache", v_cache)),
+                                torch.float8_e4m3fn, q, q_out, interleaved, status)
+    if k_cache.shape[2] != k.shape[2]:
+        raise ValueError("k_cache must be [S, Hkv, 256]")
+    k_seen, v_seen = _seen_args(k, k_seen, v_seen, want_seen)
+    _device_call(k.device, stream, _lib.qsa_kv_append_fp8, ctypes.byref(shape), _ptr(q), _ptr(q_out), _ptr(k),
+                 _ptr(v), _ptr(cos_sin), _ptr(positions), _ptr(slots), float(k_scale), float(v_scale),
+                 _ptr(k_cache), _ptr(v_cache), _ptr(k_seen), _ptr(v_seen), _ptr(status))
+    return q_out, k_seen, v_seen
+
+
+def kv_append_fp4(k, v, positions, slots, cos_sin, cache: Fp4Cache, k_scale: float, v_scale: float, q=None,
+                  q_out=None, interleaved: bool = False, k_seen=None, v_seen=None, want_seen: bool = False,
+                  status=None, stream=None):
+    """kv_append to a 4-bit cache.  k_scale (v_scale) is the tensor's FP32
+    scale, about max|k| / 2688 so that the block scales use E4M3's range.
+    Returns (q_out, k_seen, v_seen) as kv_append_fp8."""
+    buf = cache.buffer
+    shape, q_out = _append_args(k, v, positions, slots, cos_sin, (("cache", buf),), torch.uint8, q, q_out,
+                                interleaved, status)
+    shape.bscale_stride_slot, shape.bscale_stride_head = shape.kv_stride_slot, shape.kv_stride_head
+    k_seen, v_seen = _seen_args(k, k_seen, v_seen, want_seen)
+    b = buf.data_ptr()
+    _device_call(k.device, stream, _lib.qsa_kv_append_fp4, ctypes.byref(shape), _ptr(q), _ptr(q_out), _ptr(k),
+                 _ptr(v), _ptr(cos_sin), _ptr(positions), _ptr(slots), float(k_scale), float(v_scale), b,
+                 b + 256, b + 128, b + 272, _ptr(k_seen), _ptr(v_seen), _ptr(status))
+    return q_out, k_seen, v_seen
