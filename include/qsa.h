@@ -560,6 +560,50 @@ qsa_status_t qsa_kv_append_fp4(const qsa_append_shape_t* shape, const void* q,
                                void* v_codes, void* v_bscale, void* k_seen,
                                void* v_seen, int32_t* status, void* stream);
 
+/*
+ * Sparse attention over a 4-bit cache, as qsa_kv_append_fp4 writes it: an
+ * element of K is code * block scale * k_scale (E2M1, E4M3, FP32), of V the
+ * same with v_scale.  shape->kv_stride_slot / kv_stride_head are the byte
+ * strides of the code rows (128 bytes each), bscale_stride_* those of the
+ * block scales (16 bytes each); all multiples of 16, every base 16-byte
+ * aligned (QSA_ERR_ALIGN otherwise).  S < 2^31.  Token lists (block_size 1,
+ * last_slot NULL) or microblock lists as in qsa_sparse_prefill_block_fwd; any
+ * Q layout that qsa_shape_t allows.
+ *
+ * The rows are gathered packed and dequantised inside the SM: code * block
+ * scale has at most 6 significant bits and is exact in FP16.  Q, scaled per
+ * head by a power of two, is exact in FP16 for every element within a factor
+ * 2^31 of its head's largest |q| (smaller ones move by at most 2^-39 of that);
+ * the probabilities are rounded to FP16 (11 significant bits).  Scores, sums
+ * and outputs accumulate in FP32; k_scale multiplies the softmax scale and
+ * v_scale the normalised output.  A NaN block scale in a row that a list
+ * names, or a NaN in q, gives NaN where the formula does; infinite query
+ * elements give unspecified results for their head.  Rows that no live entry
+ * names are never read.  Other arguments and conventions as
+ * qsa_sparse_prefill_block_fwd.
+ */
+qsa_status_t qsa_sparse_prefill_fp4_fwd(
+    const qsa_shape_t* shape, int32_t block_size, const int32_t* last_slot,
+    const void* q, const void* k_codes, const void* k_bscale,
+    const void* v_codes, const void* v_bscale, int64_t bscale_stride_slot,
+    int64_t bscale_stride_head, const int32_t* topk_idx,
+    const int32_t* n_valid, float scale, float k_scale, float v_scale,
+    void* out, float* lse, int32_t* status, void* stream);
+
+/*
+ * Split-K decode over a 4-bit cache: qsa_sparse_decode_fwd's chunking,
+ * workspace (qsa_sparse_decode_workspace_bytes) and log-sum-exp merge, with
+ * the chunks computed by the kernel of qsa_sparse_prefill_fp4_fwd over token
+ * lists.
+ */
+qsa_status_t qsa_sparse_decode_fp4_fwd(
+    const qsa_shape_t* shape, const void* q, const void* k_codes,
+    const void* k_bscale, const void* v_codes, const void* v_bscale,
+    int64_t bscale_stride_slot, int64_t bscale_stride_head,
+    const int32_t* topk_idx, const int32_t* n_valid, float scale,
+    float k_scale, float v_scale, void* out, float* lse, int32_t* status,
+    int32_t num_splits, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* qsa_status_string(qsa_status_t status);
 

@@ -37,7 +37,8 @@ EXPORTS = ("qsa_sparse_prefill_fwd", "qsa_sparse_prefill_fwd_with", "qsa_sparse_
            "qsa_sparse_prefill_fwd_host", "qsa_sparse_decode_fwd", "qsa_sparse_decode_workspace_bytes",
            "qsa_sparse_decode_num_splits", "qsa_sparse_decode_fwd_noalloc",
            "qsa_sparse_prefill_fp8_fwd", "qsa_sparse_decode_fp8_fwd", "qsa_indexer_scores",
-           "qsa_indexer_fold_heads", "qsa_topk_select", "qsa_kv_append", "qsa_kv_append_fp8", "qsa_kv_append_fp4", "qsa_status_string", "qsa_abi_version")
+           "qsa_indexer_fold_heads", "qsa_topk_select", "qsa_kv_append", "qsa_kv_append_fp8", "qsa_kv_append_fp4",
+           "qsa_sparse_prefill_fp4_fwd", "qsa_sparse_decode_fp4_fwd", "qsa_status_string", "qsa_abi_version")
 
 
 class Shape(ctypes.Structure):
@@ -152,6 +153,11 @@ _lib.qsa_topk_select.argtypes = [ctypes.POINTER(IndexerShape), _vp, _vp, _vp, ct
 _lib.qsa_kv_append.argtypes = [ctypes.POINTER(AppendShape)] + [_vp] * 11
 _lib.qsa_kv_append_fp8.argtypes = ([ctypes.POINTER(AppendShape)] + [_vp] * 7 + [ctypes.c_float] * 2 + [_vp] * 6)
 _lib.qsa_kv_append_fp4.argtypes = ([ctypes.POINTER(AppendShape)] + [_vp] * 7 + [ctypes.c_float] * 2 + [_vp] * 8)
+_lib.qsa_sparse_prefill_fp4_fwd.argtypes = ([ctypes.POINTER(Shape), ctypes.c_int32] + [_vp] * 6 + [ctypes.c_int64] * 2
+                                            + [_vp] * 2 + [ctypes.c_float] * 3 + [_vp] * 4)
+_lib.qsa_sparse_decode_fp4_fwd.argtypes = ([ctypes.POINTER(Shape)] + [_vp] * 5 + [ctypes.c_int64] * 2 + [_vp] * 2
+                                           + [ctypes.c_float] * 3 + [_vp] * 3
+                                           + [ctypes.c_int32, _vp, ctypes.c_size_t, _vp])
 _lib.qsa_status_string.restype = ctypes.c_char_p
 _lib.qsa_status_string.argtypes = [ctypes.c_int]
 _lib.qsa_abi_version.restype = ctypes.c_int32
@@ -866,3 +872,83 @@ def kv_append_fp4(k, v, positions, slots, cos_sin, cache: Fp4Cache, k_scale: flo
                  _ptr(v), _ptr(cos_sin), _ptr(positions), _ptr(slots), float(k_scale), float(v_scale), b,
                  b + 256, b + 128, b + 272, _ptr(k_seen), _ptr(v_seen), _ptr(status))
     return q_out, k_seen, v_seen
+
+
+def _fp4_attention_args(q, cache: Fp4Cache, topk_idx, n_valid, out, lse, status, want_lse):
+    """Checks, outputs and the shape descriptor of an attention call over a 4-bit cache."""
+    dev = q.device
+    buf = cache.buffer
+    _need(q, "q", torch.bfloat16, dev)
+    _need(buf, "cache", torch.uint8, dev)
+    _need(topk_idx, "topk_idx", torch.int32, dev)
+    if q.dim() != 3 or topk_idx.dim() != 3:
+        raise ValueError("q and topk_idx must be 3-d")
+    T, Hq, Dh = q.shape
+    S, Hkv, _ = buf.shape
+    K = topk_idx.shape[2]
+    if topk_idx.shape[0] != T or topk_idx.shape[1] != Hkv:
+        raise ValueError("topk_idx must be [T, Hkv, K]")
+    if n_valid is not None:
+        _need(n_valid, "n_valid", torch.int32, dev)
+        if not n_valid.is_contiguous() or n_valid.shape != (T, Hkv):
+            raise ValueError("n_valid must be a contiguous [T, Hkv] tensor")
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _need(out, "out", torch.bfloat16, dev)
+        if out.shape != q.shape:
+            raise ValueError("out must be [T, Hq, D]")
+    if q.stride(2) != 1 or out.stride(2) != 1 or (K > 1 and topk_idx.stride(2) != 1):
+        raise ValueError("innermost dimensions must be contiguous")
+    if lse is None:
+        if want_lse:
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    else:
+        _need(lse, "lse", torch.float32, dev)
+        if lse.shape != (T, Hq) or (Hq > 1 and lse.stride(1) != 1):
+            raise ValueError("lse must be [T, Hq] with unit head stride")
+    if status is not None:
+        _need(status, "status", torch.int32, dev)
+    shape = Shape(T, Hq, Hkv, Dh, K, S, q.stride(0), q.stride(1), buf.stride(0), buf.stride(1), topk_idx.stride(0),
+                  topk_idx.stride(1), out.stride(0), out.stride(1), lse.stride(0) if lse is not None else Hq)
+    b = buf.data_ptr()
+    return shape, (b, b + 256, b + 128, b + 272, buf.stride(0), buf.stride(1)), out, lse
+
+
+def sparse_prefill_fp4_fwd(q, cache: Fp4Cache, topk_idx, k_scale: float, v_scale: float, n_valid=None,
+                           scale: float = 0.0, block_size: int = 1, last_slot=None, out=None, lse=None, status=None,
+                           stream=None, want_lse: bool = True):
+    """Sparse prefill over a 4-bit cache (kv_append_fp4 writes it, with the
+    same k_scale and v_scale).  Token lists (block_size 1) or microblock lists
+    with an optional last_slot [T] int32.  Returns (out, lse)."""
+    shape, cargs, out, lse = _fp4_attention_args(q, cache, topk_idx, n_valid, out, lse, status, want_lse)
+    if last_slot is not None:
+        _need_tok(last_slot, "last_slot", q.shape[0], q.device)
+    _device_call(q.device, stream, _lib.qsa_sparse_prefill_fp4_fwd, ctypes.byref(shape), int(block_size),
+                 _ptr(last_slot), _ptr(q), *cargs, _ptr(topk_idx), _ptr(n_valid), float(scale), float(k_scale),
+                 float(v_scale), _ptr(out), _ptr(lse), _ptr(status))
+    return out, lse
+
+
+def sparse_decode_fp4_fwd(q, cache: Fp4Cache, topk_idx, k_scale: float, v_scale: float, n_valid=None,
+                          scale: float = 0.0, num_splits: int = 0, workspace=None, out=None, lse=None, status=None,
+                          stream=None, want_lse: bool = True):
+    """Split-K decode over a 4-bit cache.  A workspace (see
+    decode_workspace_bytes) is allocated when none is given.  Returns (out, lse)."""
+    dev = q.device
+    shape, cargs, out, lse = _fp4_attention_args(q, cache, topk_idx, n_valid, out, lse, status, want_lse)
+    ws_bytes = 0
+    if workspace is None:
+        need = _lib.qsa_sparse_decode_workspace_bytes(ctypes.byref(shape), int(num_splits))
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            ws_bytes = need
+    else:
+        _need(workspace, "workspace", workspace.dtype, dev)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _device_call(dev, stream, _lib.qsa_sparse_decode_fp4_fwd, ctypes.byref(shape), _ptr(q), *cargs, _ptr(topk_idx),
+                 _ptr(n_valid), float(scale), float(k_scale), float(v_scale), _ptr(out), _ptr(lse), _ptr(status),
+                 int(num_splits), _ptr(workspace), ws_bytes)
+    return out, lse

@@ -331,6 +331,66 @@ qsa_status_t run_lists(const qsa_shape_t* shape, int32_t block_size, const int32
   return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
 }
 
+// Attention over a 4-bit cache: one pass over token or microblock lists, or
+// (decode) the split-K form with its merge.
+struct Cache4 {
+  const void *k_codes, *k_bscale, *v_codes, *v_bscale;
+  int64_t bscale_stride_slot, bscale_stride_head;
+};
+
+qsa_status_t run_f4(const qsa_shape_t* s, int32_t block_size, const int32_t* last_slot, const void* q,
+                    const Cache4& c, const int32_t* idx, const int32_t* n_valid, float scale, float k_scale,
+                    float v_scale, void* out, float* lse, int32_t* status, bool decode, int32_t num_splits,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+  const qsa_status_t rc = validate(s, q, c.k_codes, c.v_codes, idx, out);
+  if (rc != QSA_OK) return rc;
+  if (s->num_slots > 0x7fffffffLL) return QSA_ERR_UNSUPPORTED;
+  const int shift = block_shift_of(block_size);
+  if (shift < 0) return QSA_ERR_UNSUPPORTED;
+  // keys are counted in 32 bits, up to the end of a list's last tile
+  if ((static_cast<int64_t>(s->topk) << shift) > 0x7fffffffLL - qsa::tc::kKeys) return QSA_ERR_UNSUPPORTED;
+  if (s->num_tokens > 0 && s->topk > 0) {
+    if (c.k_bscale == nullptr || c.v_bscale == nullptr) return QSA_ERR_NULL;
+    if (c.bscale_stride_slot < 0 || c.bscale_stride_head < 0) return QSA_ERR_SHAPE;
+    if (s->num_slots > 0 && c.bscale_stride_slot == 0) return QSA_ERR_SHAPE;
+    if (s->kv_stride_slot % 16 != 0 || s->kv_stride_head % 16 != 0 || c.bscale_stride_slot % 16 != 0 ||
+        c.bscale_stride_head % 16 != 0 || !aligned16(c.k_bscale) || !aligned16(c.v_bscale))
+      return QSA_ERR_ALIGN;
+  }
+  if (s->num_tokens == 0) return QSA_OK;
+  SplitPlan pl = {};
+  if (decode && !plan_splits(s, num_splits, &pl)) return QSA_ERR_CUDA;
+  const bool split = decode && pl.splits > 1;
+  if (split) {
+    if (workspace == nullptr) return QSA_ERR_NULL;
+    if (workspace_bytes < pl.total_bytes) return QSA_ERR_SHAPE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return QSA_ERR_ALIGN;
+  }
+  static thread_local qsa::f4::F4Params fp;
+  fill_tc_params(&fp.t, s, q, nullptr, nullptr, idx, n_valid, scale, k_scale, v_scale, out, lse, status, shift,
+                 last_slot);
+  fp.codes[0] = static_cast<const char*>(c.k_codes);
+  fp.codes[1] = static_cast<const char*>(c.v_codes);
+  fp.bscale[0] = static_cast<const char*>(c.k_bscale);
+  fp.bscale[1] = static_cast<const char*>(c.v_bscale);
+  fp.c_ss = s->kv_stride_slot;
+  fp.c_sh = s->kv_stride_head;
+  fp.b_ss = c.bscale_stride_slot;
+  fp.b_sh = c.bscale_stride_head;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (split) {
+    fp.t.splits = pl.splits;
+    fp.t.chunk = pl.chunk;
+    fp.t.part_o = static_cast<float*>(workspace);
+    fp.t.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.lse_offset);
+  }
+  const bool plain = shift == 0 && last_slot == nullptr;
+  if ((plain ? launch_f4<false>(fp, st) : launch_f4<true>(fp, st)) != cudaSuccess) return QSA_ERR_CUDA;
+  if (split && launch_merge(s, fp.t.part_o, fp.t.part_lse, pl.splits, out, lse, st) != cudaSuccess)
+    return QSA_ERR_CUDA;
+  return QSA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -530,6 +590,28 @@ qsa_status_t qsa_sparse_prefill_fp8_fwd(const qsa_shape_t* shape, int32_t block_
                                         float* lse, int32_t* status, void* stream) {
   return run_lists(shape, block_size, last_slot, q, k_cache, v_cache, topk_idx, n_valid, scale,
                    k_scale, v_scale, true, out, lse, status, stream);
+}
+
+qsa_status_t qsa_sparse_prefill_fp4_fwd(const qsa_shape_t* shape, int32_t block_size, const int32_t* last_slot,
+                                        const void* q, const void* k_codes, const void* k_bscale,
+                                        const void* v_codes, const void* v_bscale, int64_t bscale_stride_slot,
+                                        int64_t bscale_stride_head, const int32_t* topk_idx,
+                                        const int32_t* n_valid, float scale, float k_scale, float v_scale,
+                                        void* out, float* lse, int32_t* status, void* stream) {
+  return run_f4(shape, block_size, last_slot, q,
+                {k_codes, k_bscale, v_codes, v_bscale, bscale_stride_slot, bscale_stride_head}, topk_idx, n_valid,
+                scale, k_scale, v_scale, out, lse, status, false, 0, nullptr, 0, stream);
+}
+
+qsa_status_t qsa_sparse_decode_fp4_fwd(const qsa_shape_t* shape, const void* q, const void* k_codes,
+                                       const void* k_bscale, const void* v_codes, const void* v_bscale,
+                                       int64_t bscale_stride_slot, int64_t bscale_stride_head,
+                                       const int32_t* topk_idx, const int32_t* n_valid, float scale, float k_scale,
+                                       float v_scale, void* out, float* lse, int32_t* status, int32_t num_splits,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+  return run_f4(shape, 1, nullptr, q,
+                {k_codes, k_bscale, v_codes, v_bscale, bscale_stride_slot, bscale_stride_head}, topk_idx, n_valid,
+                scale, k_scale, v_scale, out, lse, status, true, num_splits, workspace, workspace_bytes, stream);
 }
 
 qsa_status_t qsa_sparse_prefill_debug_gather_lists(const qsa_shape_t* shape, int32_t block_size,

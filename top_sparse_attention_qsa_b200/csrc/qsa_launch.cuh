@@ -11,6 +11,7 @@
 
 #include "qsa.h"
 #include "qsa_host.cuh"
+#include "qsa_prefill_f4.cuh"
 #include "qsa_prefill_f8.cuh"
 #include "qsa_prefill_mma.cuh"
 #include "qsa_prefill_tc.cuh"
@@ -197,6 +198,24 @@ cudaError_t launch_f8(const qsa::tc::TcParams& tp, cudaStream_t stream) {
   unsigned grid = 0;
   if ((e = persistent_grid(tp, &grid)) != cudaSuccess) return e;
   kernel<<<grid, qsa::f8::kThreads8, qsa::f8::F_SMEM, stream>>>(tp);
+  return cudaGetLastError();
+}
+
+template <bool kBlocks>
+cudaError_t launch_f4(const qsa::f4::F4Params& fp, cudaStream_t stream) {
+  static std::atomic<int> done[kMaxDevices];
+  static std::atomic<int> regs_ok;
+  auto kernel = qsa::f4::qsa_prefill_f4_kernel<kBlocks>;
+  using namespace qsa::f4;
+  cudaError_t e = check_register_split(
+      kernel, kThreads4,
+      128L * (kRegsProd4 + kRegsMisc4 + kRegsKd4 + kRegsVd4 + 2L * kRegsSm4 + kRegsEpi4), &regs_ok);
+  if (e != cudaSuccess) return e;
+  e = set_smem_once(kernel, qsa::f4::H_SMEM, done);
+  if (e != cudaSuccess) return e;
+  unsigned grid = 0;
+  if ((e = persistent_grid(fp.t, &grid)) != cudaSuccess) return e;
+  kernel<<<grid, qsa::f4::kThreads4, qsa::f4::H_SMEM, stream>>>(fp);
   return cudaGetLastError();
 }
 
