@@ -361,6 +361,8 @@ qsa_status_t run_f4(const qsa_shape_t* s, int32_t block_size, const int32_t* las
   SplitPlan pl = {};
   if (decode && !plan_splits(s, num_splits, &pl)) return QSA_ERR_CUDA;
   const bool split = decode && pl.splits > 1;
+  // units are counted in 32 bits, one grid past the end included
+  if (s->num_tokens * s->num_kv_heads > (0x7fffffffLL - 65536) / (split ? pl.splits : 1)) return QSA_ERR_UNSUPPORTED;
   if (split) {
     if (workspace == nullptr) return QSA_ERR_NULL;
     if (workspace_bytes < pl.total_bytes) return QSA_ERR_SHAPE;

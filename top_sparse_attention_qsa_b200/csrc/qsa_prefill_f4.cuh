@@ -49,14 +49,17 @@ struct F4Params {
   int64_t c_ss, c_sh, b_ss, b_sh; // byte strides of the codes and of the scales
 };
 
-constexpr int kStages = 3;                          // packed tiles in each ring
+constexpr int kStages = 2;                          // packed tiles in each ring
 constexpr int kCodeBytes = kKeys * 128;             // one packed tile: codes,
 constexpr int kStageBytes = kCodeBytes + kKeys * 16;  // then block scales
 constexpr int kHalfBytes = 32768;                   // FP16 V half: 128 keys x 128 dims
-constexpr int kVHalves = 2;
-constexpr int kTkStages = 3;                        // TMEM K stages of 128 dims (64 columns)
+constexpr int kVHalves = 4;
+constexpr int kTkStages = 6;                        // TMEM K stages of 128 dims (64 columns)
+constexpr int kMasks = 8;                           // tiles whose key masks are kept
 constexpr float kPShift = 7.f;                      // P is stored times 2^7
 
+constexpr int kTmemCols4 = 512;
+constexpr int kUS = 0, kUO = 32, kUK = 96;         // S: 2 x 16; O: 2 units x 2 halves x 16; K stages of 64
 constexpr int H_K = 0;
 constexpr int H_V = H_K + kStages * kStageBytes;
 constexpr int H_VH = H_V + kStages * kStageBytes;
@@ -65,7 +68,9 @@ constexpr int H_P = H_Q + 2 * kQBytes;
 constexpr int H_QSC = H_P + 2 * kPBytes;            // 2 buffers x 16 per-head score factors
 constexpr int H_RED = H_QSC + 2 * kGp * 4;          // max[4][16], votes[2][8], sum[2][4][16]
 constexpr int H_LM = H_RED + 1024;                  // per unit parity: l[16], m[16]
-constexpr int H_BAR = H_LM + 256;
+constexpr int H_MASK = H_LM + 256;                  // kMasks x 4 words: bit = key of the quadrant counts
+constexpr int H_BAR = H_MASK + kMasks * 16;
+static_assert(kUK + 64 * kTkStages <= kTmemCols4, "TMEM columns");
 static_assert(H_VH % 1024 == 0 && H_Q % 1024 == 0 && kStageBytes % 1024 == 0, "swizzle atoms");
 constexpr int J_KF = 0, J_KE = J_KF + kStages, J_VF = J_KE + kStages, J_VE = J_VF + kStages, J_TKF = J_VE + kStages,
               J_TKE = J_TKF + kTkStages, J_VHF = J_TKE + kTkStages, J_VHE = J_VHF + kVHalves, J_SF = J_VHE + kVHalves,
@@ -76,8 +81,6 @@ constexpr int H_MISC = H_BAR + J_NUM * 8;           // tmem base, abort flag
 constexpr int H_SMEM = H_MISC + 16 + 1024;
 static_assert(H_SMEM <= 232448, "shared memory");
 
-constexpr int kTmemCols4 = 512;
-constexpr int kUS = 0, kUO = 32, kUK = 128;         // S: 2 x 16; O: 2 units x 2 halves x 16; K stages of 64
 
 // kind::f16 with FP16 A and B (formats 0), FP32 accumulator, M = 128, N = 16.
 constexpr uint32_t kIdescQK4 = (1u << 4) | (2u << 17) | (8u << 24);
@@ -103,18 +106,6 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
 
@@ -151,20 +142,63 @@ __device__ __forceinline__ void scale_pairs(uint32_t two_bytes, __half2& s0, __h
   s1 = __high2half2(v);
 }
 
+// ------------------------------------------------------------------ units
+
+// The CTA's units blockIdx.x, + gridDim.x, ... in decode_unit's order, carried
+// in 32 bits from one to the next (the host refuses 2^31 - gridDim units or
+// more): 64-bit divisions in every warp were a sixth of all instructions.
+struct Walk {
+  uint32_t per_head, rem, g, left;     // left: units still to do, this one included
+  __device__ explicit Walk(const TcParams& p) {
+    per_head = static_cast<uint32_t>(p.T) * p.splits;
+    const uint32_t units = per_head * p.Hkv;
+    g = blockIdx.x / per_head;
+    rem = blockIdx.x - g * per_head;
+    left = blockIdx.x < units ? (units - blockIdx.x + gridDim.x - 1) / gridDim.x : 0u;
+  }
+  __device__ bool more() const { return left != 0u; }
+  __device__ void next() {
+    --left;
+    rem += gridDim.x;
+    while (rem >= per_head && left != 0u) {
+      rem -= per_head;
+      ++g;
+    }
+  }
+  __device__ Unit unit(const TcParams& p) const {
+    Unit r;
+    const uint32_t t = p.splits == 1 ? rem : rem / static_cast<uint32_t>(p.splits);
+    r.g = static_cast<int>(g);
+    r.t = t;
+    r.s = static_cast<int>(rem - t * p.splits);
+    int n = p.K;
+    if (p.n_valid != nullptr) n = min(n, max(__ldg(p.n_valid + r.t * p.Hkv + r.g), 0));
+    r.j0 = r.s * p.chunk;
+    r.n_eff = max(0, min((n << p.block_shift) - r.j0, p.chunk));
+    r.n_tiles = (r.n_eff + kKeys - 1) / kKeys;
+    return r;
+  }
+};
+
 // ------------------------------------------------------------------ producers
 
 // Warp pw copies rows 32 pw .. 32 pw + 31 of every tile: 8 lanes per code row
 // (four rows per instruction), then each lane its own row's scales.
+// Which keys count goes to the softmax warps as one ballot word per quadrant,
+// in a ring of kMasks tiles: a tile's K stage is refilled only once K tile c -
+// kStages is in TMEM, which runs at most kTkStages / 2 tiles ahead of the
+// scores, and those at most two ahead of the softmax's reads (with the S it
+// has handed back): kStages + kTkStages / 2 + 2 < kMasks.
+static_assert(kStages + kTkStages / 2 + 2 < kMasks, "key masks");
 template <bool kBlocks>
-__device__ void producer4(const F4Params& fp, const Sync& sy, uint32_t sb, int pw, int lane) {
+__device__ void producer4(const F4Params& fp, const Sync& sy, uint32_t sb, uint8_t* sp, int pw, int lane) {
   const TcParams& p = fp.t;
   uint32_t c_tile = 0;
-  const int64_t units = num_units(p);
   const int cc = lane & 7, rsel = lane >> 3;
   const int r_own = 32 * pw + lane;
   bool ok = true;
-  for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
-    const Unit un = decode_unit(p, u);
+  for (Walk wk(p); wk.more() && ok; wk.next()) {
+    const Unit un = wk.unit(p);
     const int32_t* list = p.idx + un.t * p.idx_st + static_cast<int64_t>(un.g) * p.idx_sh;
     const int32_t last = kBlocks ? last_visible(p, un.t) : 0x7fffffff;
     const int64_t hc = static_cast<int64_t>(un.g) * fp.c_sh + cc * 16, hb = static_cast<int64_t>(un.g) * fp.b_sh;
@@ -192,6 +226,13 @@ __device__ void producer4(const F4Params& fp, const Sync& sy, uint32_t sb, int p
         }
         const char* sb0 = fp.bscale[kv] + hb + (id >= 0 ? static_cast<int64_t>(id) * fp.b_ss : int64_t(0));
         cp_async_16(dst + kCodeBytes + r_own * 16, sb0, id >= 0 ? 16 : 0);
+        if (kv == 0) {
+          const uint32_t mask = __ballot_sync(0xffffffffu, id >= 0);
+          if (lane == 0) {
+            reinterpret_cast<volatile uint32_t*>(sp + H_MASK)[(c_tile % kMasks) * 4 + pw] = mask;
+            mbar_arrive(sy.bar(J_KF + slot));
+          }
+        }
         cp_async_mbar_arrive(sy.bar((kv ? J_VF : J_KF) + slot));
       }
     }
@@ -206,40 +247,38 @@ __device__ void producer4(const F4Params& fp, const Sync& sy, uint32_t sb, int p
 __device__ void k_dequant(const F4Params& fp, const Sync& sy, uint32_t sb, uint32_t tmem, int warp, int lane) {
   const TcParams& p = fp.t;
   uint32_t c_tile = 0, c_half = 0;
-  const int64_t units = num_units(p);
   const int row = (warp & 3) * 32 + lane;
   const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kUK;
   bool ok = true;
-  for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
-    const Unit un = decode_unit(p, u);
+  for (Walk wk(p); wk.more() && ok; wk.next()) {
+    const Unit un = wk.unit(p);
     for (int i = 0; i < un.n_tiles && ok; ++i, ++c_tile) {
       const uint32_t slot = c_tile % kStages;
       ok = sy.wait_warp(J_KF + slot, (c_tile / kStages) & 1u);
       if (!ok) break;
       const uint32_t src = sb + H_K + slot * kStageBytes;
       const uint4 sc = ld_shared_v4(src + kCodeBytes + row * 16);
-      const uint32_t scw[4] = {sc.x, sc.y, sc.z, sc.w};
-#pragma unroll
+#pragma unroll 1
       for (int h = 0; h < 2; ++h, ++c_half) {
         const uint32_t st = c_half % kTkStages;
         ok = sy.wait_warp(J_TKE + st, ((c_half / kTkStages) & 1u) ^ 1u);
         if (!ok) break;
         tc_fence_after();
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {                  // 64 dims: two 16-byte chunks, 4 block scales
-          uint32_t out[32];
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const int ch = 4 * h + 2 * q + c;
-            const uint4 w = ld_shared_v4(src + row * 128 + ((ch ^ (row & 7)) << 4));
-            __half2 s0, s1;
-            scale_pairs((scw[ch >> 1] >> (16 * (ch & 1))) & 0xffffu, s0, s1);
-            dequant8(w.x, s0, out + 16 * c);
-            dequant8(w.y, s0, out + 16 * c + 4);
-            dequant8(w.z, s1, out + 16 * c + 8);
-            dequant8(w.w, s1, out + 16 * c + 12);
-          }
-          tmem_st32(tl + st * 64 + q * 32, out);
+        uint32_t s01 = h ? sc.z : sc.x, s23 = h ? sc.w : sc.y;
+        // kept rolled: with every role's loops unrolled the warps waited for
+        // instructions more than for anything else
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {                  // 32 dims: one 16-byte chunk, two block scales
+          const uint4 w = ld_shared_v4(src + row * 128 + (((4 * h + c) ^ (row & 7)) << 4));
+          __half2 s0, s1;
+          scale_pairs(s01 & 0xffffu, s0, s1);
+          s01 = c == 1 ? s23 : s01 >> 16;
+          uint32_t out[16];
+          dequant8(w.x, s0, out);
+          dequant8(w.y, s0, out + 4);
+          dequant8(w.z, s1, out + 8);
+          dequant8(w.w, s1, out + 12);
+          tmem_st16(tl + st * 64 + c * 16, out);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -257,37 +296,37 @@ __device__ void k_dequant(const F4Params& fp, const Sync& sy, uint32_t sb, uint3
 __device__ void v_dequant(const F4Params& fp, const Sync& sy, uint32_t sb, int warp, int lane) {
   const TcParams& p = fp.t;
   uint32_t c_tile = 0, c_half = 0;
-  const int64_t units = num_units(p);
   const int row = (warp & 3) * 32 + lane;
   bool ok = true;
-  for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
-    const Unit un = decode_unit(p, u);
+  for (Walk wk(p); wk.more() && ok; wk.next()) {
+    const Unit un = wk.unit(p);
     for (int i = 0; i < un.n_tiles && ok; ++i, ++c_tile) {
       const uint32_t slot = c_tile % kStages;
       ok = sy.wait_warp(J_VF + slot, (c_tile / kStages) & 1u);
       if (!ok) break;
       const uint32_t src = sb + H_V + slot * kStageBytes;
       const uint4 sc = ld_shared_v4(src + kCodeBytes + row * 16);
-      const uint32_t scw[4] = {sc.x, sc.y, sc.z, sc.w};
-#pragma unroll
+#pragma unroll 1
       for (int h = 0; h < 2; ++h, ++c_half) {
         const uint32_t st = c_half % kVHalves;
         ok = sy.wait_warp(J_VHE + st, ((c_half / kVHalves) & 1u) ^ 1u);
         if (!ok) break;
         const uint32_t dst = sb + H_VH + st * kHalfBytes + row * 128;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int ch = 4 * h + c;                    // 32 dims: FP16 chunks 4 c .. 4 c + 3 of the half
-          const uint4 w = ld_shared_v4(src + row * 128 + ((ch ^ (row & 7)) << 4));
+        uint32_t s01 = h ? sc.z : sc.x, s23 = h ? sc.w : sc.y;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {                  // 32 dims: FP16 chunks 4 c .. 4 c + 3 of the half
+          const uint4 w = ld_shared_v4(src + row * 128 + (((4 * h + c) ^ (row & 7)) << 4));
           __half2 s0, s1;
-          scale_pairs((scw[ch >> 1] >> (16 * (ch & 1))) & 0xffffu, s0, s1);
+          scale_pairs(s01 & 0xffffu, s0, s1);
+          s01 = c == 1 ? s23 : s01 >> 16;
           const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+          const uint32_t blk = dst + (c >> 1) * kBlockBytes;
+          const int c0 = 4 * (c & 1);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t o[4];
             dequant8(ws[j], j < 2 ? s0 : s1, o);
-            const int cf = 4 * c + j;
-            st_shared_v4(dst + (cf >> 3) * kBlockBytes + (((cf & 7) ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
+            st_shared_v4(blk + (((c0 + j) ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
           }
         }
         fence_proxy_async_smem();
@@ -345,10 +384,9 @@ __device__ __forceinline__ void q_tile(const TcParams& p, const Unit& un, uint32
 
 __device__ void q4(const TcParams& p, const Sync& sy, uint32_t sb, uint8_t* sp, int lane) {
   uint32_t c_unit = 0;
-  const int64_t units = num_units(p);
   bool ok = true;
-  for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
-    const Unit un = decode_unit(p, u);
+  for (Walk wk(p); wk.more() && ok; wk.next()) {
+    const Unit un = wk.unit(p);
     const uint32_t qb = c_unit & 1u;
     ok = sy.wait_warp(J_QE + qb, ((c_unit >> 1) & 1u) ^ 1u);
     if (!ok) break;
@@ -368,10 +406,9 @@ __device__ void q4(const TcParams& p, const Sync& sy, uint32_t sb, uint8_t* sp, 
 
 __device__ void qk4(const TcParams& p, const Sync& sy, uint32_t sb, uint32_t tmem) {
   uint32_t c_tile = 0, c_half = 0, c_unit = 0;
-  const int64_t units = num_units(p);
   bool ok = true;
-  for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
-    const Unit un = decode_unit(p, u);
+  for (Walk wk(p); wk.more() && ok; wk.next()) {
+    const Unit un = wk.unit(p);
     const uint32_t qb = c_unit & 1u;
     if (un.n_tiles > 0) ok = sy.wait(J_QF + qb, (c_unit >> 1) & 1u);
     if (!ok) break;
@@ -405,10 +442,9 @@ __device__ void qk4(const TcParams& p, const Sync& sy, uint32_t sb, uint32_t tme
 
 __device__ void pv4(const TcParams& p, const Sync& sy, uint32_t sb, uint32_t tmem) {
   uint32_t c_tile = 0, c_half = 0, c_unit = 0;
-  const int64_t units = num_units(p);
   bool ok = true;
-  for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
-    const Unit un = decode_unit(p, u);
+  for (Walk wk(p); wk.more() && ok; wk.next()) {
+    const Unit un = wk.unit(p);
     const uint32_t ue = c_unit++;
     const uint32_t ob = ue & 1u;
     ok = sy.wait(J_OE + ob, ((ue >> 1) & 1u) ^ 1u);
@@ -445,20 +481,11 @@ __device__ void pv4(const TcParams& p, const Sync& sy, uint32_t sb, uint32_t tme
 
 // ------------------------------------------------------------------ softmax
 
-// p = 2^(s - m + 7) for this thread's key and 8 heads, as FP16 pairs; pv gets
-// the unrounded p.  A NaN score gives a NaN p.
-__device__ __forceinline__ void form_p4(const float (&s)[kHpw4], const float (&m)[kHpw4], uint32_t (&pk)[4],
-                                        float (&pv)[kHpw4]) {
-#pragma unroll
-  for (int h = 0; h < kHpw4; ++h) pv[h] = ex2(s[h] - (m[h] == -INFINITY ? 0.f : m[h] - kPShift));
-#pragma unroll
-  for (int h = 0; h < kHpw4; h += 2) pk[h >> 1] = pack_f16x2(pv[h], pv[h + 1]);
-}
-
 // Softmax warp w: TMEM lane quadrant w & 3 (thread = key of the tile), heads
-// [8 hh, 8 hh + 8).  The votes, the exact path and the sums are those of the
-// FP8 kernel.
-template <bool kBlocks>
+// [8 hh, 8 hh + 8).  x = s - mx with mx = m - 7 (m the running max), so that
+// p = 2^x is the probability times 2^7 and x > 15 means the lazy rescale's
+// bound is passed.  The votes, the exact path and the sums are those of the
+// FP8 kernel.  Heads past the group have a score factor 0 and mx = +inf.
 __device__ void softmax4(const TcParams& p, const Sync& sy, uint32_t sb, uint8_t* sp, uint32_t tmem, int warp,
                          int lane) {
   const int wq = warp & 3;
@@ -470,61 +497,57 @@ __device__ void softmax4(const TcParams& p, const Sync& sy, uint32_t sb, uint8_t
   uint8_t* votes = sp + H_RED + 256;
   float* red_sum = red_max + 128;
   const float* qsc_all = reinterpret_cast<const float*>(sp + H_QSC);
+  const volatile uint32_t* masks = reinterpret_cast<const volatile uint32_t*>(sp + H_MASK) + wq;
+  constexpr float kOver = kRescaleLog2 + kPShift;
   uint32_t c_tile = 0, c_unit = 0, c_exact = 0;
   uint32_t vote_par = 0u;
-  const int64_t units = num_units(p);
-  const int G = p.G;
   bool ok = true;
-  for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
-    const Unit un = decode_unit(p, u);
-    const int32_t* list = p.idx + un.t * p.idx_st + static_cast<int64_t>(un.g) * p.idx_sh;
-    const int32_t last = kBlocks ? last_visible(p, un.t) : 0x7fffffff;
+  for (Walk wk(p); wk.more() && ok; wk.next()) {
+    const Unit un = wk.unit(p);
     const uint32_t qb = c_unit & 1u;
     ok = sy.wait_warp(J_QF + qb, (c_unit >> 1) & 1u);
     if (!ok) break;
-    float qs[kHpw4];
-#pragma unroll
-    for (int h = 0; h < kHpw4; ++h) qs[h] = qsc_all[qb * kGp + h0 + h];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(sy.bar(J_QE + qb));
-    float m_run[kHpw4], l_part[kHpw4];
+    float qs[kHpw4], mx[kHpw4], l_part[kHpw4];
 #pragma unroll
     for (int h = 0; h < kHpw4; ++h) {
-      m_run[h] = -INFINITY;
+      qs[h] = h0 + h < p.G ? qsc_all[qb * kGp + h0 + h] : 0.f;
+      mx[h] = h0 + h < p.G ? -INFINITY : INFINITY;     // no key seen; never one
       l_part[h] = 0.f;
     }
-    int32_t entry_next = un.n_tiles > 0 ? key_entry<kBlocks>(p, list, un, key) : -1;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(sy.bar(J_QE + qb));
     for (int i = 0; i < un.n_tiles; ++i) {
       const uint32_t c = c_tile + i;
       const uint32_t buf = c & 1u;
-      const bool valid = key_slot<kBlocks>(p, un, i * kKeys + key, entry_next, last) >= 0;
-      entry_next = i + 1 < un.n_tiles ? key_entry<kBlocks>(p, list, un, (i + 1) * kKeys + key) : -1;
       ok = sy.wait_warp(J_SF + buf, (c >> 1) & 1u);
       if (!ok) break;
       tc_fence_after();
       uint32_t r8[8];
       tmem_ld8(tl + kUS + buf * 16 + 8 * hh, r8);
+      const bool valid = (masks[(c % kMasks) * 4] >> lane) & 1u;
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(sy.bar(J_SE + buf));
-      float s[kHpw4];
-      bool over = false;
-#pragma unroll
-      for (int h = 0; h < kHpw4; ++h) {
-        s[h] = (valid && h0 + h < G) ? __uint_as_float(r8[h]) * qs[h] : -INFINITY;
-        over |= s[h] > m_run[h] + kRescaleLog2;
-      }
-      uint32_t pk[4];
-      float pv[kHpw4];
+      float x[kHpw4];
       bool exact = true;
       if (i > 0) {
-        const bool wover = __any_sync(0xffffffffu, over);
+        float top = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < kHpw4; ++h) {
+          // a head without a key yet has mx = -inf and takes the exact path
+          x[h] = valid ? fmaf(__uint_as_float(r8[h]), qs[h], -mx[h]) : -INFINITY;
+          top = fmaxf(top, x[h]);
+        }
+        const bool wover = __any_sync(0xffffffffu, top > kOver);
         uint8_t* vt = votes + buf * 8;
         if (lane == 0) vt[warp - kWarpSm4] = wover ? 1 : 0;
         __syncwarp();
         if (lane == 0) mbar_arrive(sy.bar(J_RMAX + buf));
-        if (!wover) form_p4(s, m_run, pk, pv);
+        if (!wover) {
+#pragma unroll
+          for (int h = 0; h < kHpw4; ++h) x[h] = ex2(x[h]);
+        }
         ok = sy.wait_warp(J_RMAX + buf, (vote_par >> buf) & 1u);
         vote_par ^= 1u << buf;
         if (!ok) break;
@@ -532,6 +555,9 @@ __device__ void softmax4(const TcParams& p, const Sync& sy, uint32_t sb, uint8_t
         exact = (vw.x | vw.y) != 0u;
       }
       if (exact) {
+        float s[kHpw4];
+#pragma unroll
+        for (int h = 0; h < kHpw4; ++h) s[h] = valid && h0 + h < p.G ? __uint_as_float(r8[h]) * qs[h] : -INFINITY;
         const float wmax = xreduce8<true>(s, lane);
         float* rm = red_max;
         if ((lane & 3) == 0) rm[wq * 16 + h0 + ((lane >> 2) & 7)] = wmax;
@@ -540,51 +566,51 @@ __device__ void softmax4(const TcParams& p, const Sync& sy, uint32_t sb, uint8_t
         ok = sy.wait_warp(J_RMX2, c_exact & 1u);
         ++c_exact;
         if (!ok) break;
-        float tmax[kHpw4];
-#pragma unroll
-        for (int h = 0; h < kHpw4; ++h)
-          tmax[h] = fmaxf(fmaxf(rm[h0 + h], rm[16 + h0 + h]), fmaxf(rm[32 + h0 + h], rm[48 + h0 + h]));
+        float tmax[kHpw4];                             // the tile's max, less 7
         bool need = false;
 #pragma unroll
-        for (int h = 0; h < kHpw4; ++h)
-          need |= (m_run[h] != -INFINITY) && (tmax[h] > m_run[h] + kRescaleLog2);
-        if (need) {
-          if (i > 0) {
-            const uint32_t cp = c - 1;
-            ok = sy.wait_warp(J_PE + (cp & 1u), (cp >> 1) & 1u);
-            if (!ok) break;
-          }
+        for (int h = 0; h < kHpw4; ++h) {
+          tmax[h] = fmaxf(fmaxf(rm[h0 + h], rm[16 + h0 + h]), fmaxf(rm[32 + h0 + h], rm[48 + h0 + h])) - kPShift;
+          need |= (mx[h] != -INFINITY) && (tmax[h] > mx[h] + kRescaleLog2);
+        }
+        if (need) {                                    // (never on a unit's first tile: no head has a max yet)
+          const uint32_t cp = c - 1;
+          ok = sy.wait_warp(J_PE + (cp & 1u), (cp >> 1) & 1u);
+          if (!ok) break;
           tc_fence_after();
           float alpha[kHpw4];
 #pragma unroll
           for (int h = 0; h < kHpw4; ++h) {
-            const float mn = fmaxf(m_run[h], tmax[h]);
-            alpha[h] = m_run[h] == -INFINITY ? 1.f : ex2(m_run[h] - mn);
-            m_run[h] = mn;
+            const float mn = fmaxf(mx[h], tmax[h]);
+            alpha[h] = mx[h] == mn ? 1.f : ex2(mx[h] - mn);
+            mx[h] = mn;
             l_part[h] *= alpha[h];
           }
-          if (i > 0) {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint32_t o[8];
-              const uint32_t col = kUO + (c_unit & 1u) * 32 + half * 16 + 8 * hh;
-              tmem_ld8(tl + col, o);
-              tmem_wait_ld();
+          for (int half = 0; half < 2; ++half) {
+            uint32_t o[8];
+            const uint32_t col = kUO + (c_unit & 1u) * 32 + half * 16 + 8 * hh;
+            tmem_ld8(tl + col, o);
+            tmem_wait_ld();
 #pragma unroll
-              for (int h = 0; h < kHpw4; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * alpha[h]);
-              tmem_st8(tl + col, o);
-            }
-            tmem_wait_st();
+            for (int h = 0; h < kHpw4; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * alpha[h]);
+            tmem_st8(tl + col, o);
           }
+          tmem_wait_st();
         } else {
 #pragma unroll
           for (int h = 0; h < kHpw4; ++h)
-            if (m_run[h] == -INFINITY) m_run[h] = tmax[h];
+            if (mx[h] == -INFINITY) mx[h] = tmax[h];
         }
-        form_p4(s, m_run, pk, pv);
-      }
+        // still no key of this head: every s is -inf and p = 0
 #pragma unroll
-      for (int h = 0; h < kHpw4; ++h) l_part[h] += pv[h];
+        for (int h = 0; h < kHpw4; ++h) x[h] = ex2(s[h] - (mx[h] == -INFINITY ? 0.f : mx[h]));
+      }
+      uint32_t pk[4];
+#pragma unroll
+      for (int h = 0; h < kHpw4; h += 2) pk[h >> 1] = pack_f16x2(x[h], x[h + 1]);
+#pragma unroll
+      for (int h = 0; h < kHpw4; ++h) l_part[h] += x[h];
       ok = sy.wait_warp(J_PE + buf, ((c >> 1) & 1u) ^ 1u);
       if (!ok) break;
       st_shared_v4(sb + H_P + buf * kPBytes + hh * 2048 + key * 16, pk[0], pk[1], pk[2], pk[3]);
@@ -610,7 +636,7 @@ __device__ void softmax4(const TcParams& p, const Sync& sy, uint32_t sb, uint8_t
         float mk = 0.f;
 #pragma unroll
         for (int h = 0; h < kHpw4; ++h)
-          if (h == lane) mk = m_run[h];
+          if (h == lane) mk = mx[h];
         const int h = h0 + lane;
         lm[h] = (rs[h] + rs[16 + h]) + (rs[32 + h] + rs[48 + h]);
         lm[16 + h] = mk;
@@ -630,11 +656,10 @@ __device__ void epilogue4(const TcParams& p, const Sync& sy, uint8_t* sp, uint32
   const int key = wq * 32 + lane;
   const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32) << 16);
   uint32_t c_unit = 0;
-  const int64_t units = num_units(p);
   const int G = p.G;
   bool ok = true;
-  for (int64_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
-    const Unit un = decode_unit(p, u);
+  for (Walk wk(p); wk.more() && ok; wk.next()) {
+    const Unit un = wk.unit(p);
     const uint32_t ub = c_unit & 1u, par = (c_unit >> 1) & 1u;
     ++c_unit;
     ok = sy.wait_warp(J_LF + ub, par);
@@ -643,8 +668,7 @@ __device__ void epilogue4(const TcParams& p, const Sync& sy, uint8_t* sp, uint32
     const int64_t row0 = un.t * static_cast<int64_t>(p.Hkv) * G + static_cast<int64_t>(un.g) * G;
     if (wq == 0 && lane < G && (p.lse != nullptr || p.part_lse != nullptr)) {
       const float lk = lm[lane], mk = lm[16 + lane];
-      const float lv = lk == 0.f ? -INFINITY
-                                 : ((mk == -INFINITY ? 0.f : mk - kPShift) + lg2(lk)) * 0.69314718055994531f;
+      const float lv = lk == 0.f ? -INFINITY : (mk + lg2(lk)) * 0.69314718055994531f;
       if (p.part_lse != nullptr)
         p.part_lse[(row0 + lane) * p.splits + un.s] = lv;
       else
@@ -704,7 +728,7 @@ __global__ void __launch_bounds__(kThreads4, 1) qsa_prefill_f4_kernel(const __gr
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(sy.bar(J_KF + s), 128);
+      mbar_init(sy.bar(J_KF + s), 128 + 4);         // every lane's copies; each warp's key mask
       mbar_init(sy.bar(J_KE + s), 4);
       mbar_init(sy.bar(J_VF + s), 128);
       mbar_init(sy.bar(J_VE + s), 4);
@@ -747,7 +771,7 @@ __global__ void __launch_bounds__(kThreads4, 1) qsa_prefill_f4_kernel(const __gr
 
   if (warp < kWarpMisc4) {
     setmaxnreg_dec<kRegsProd4>();
-    producer4<kBlocks>(fp, sy, sb, warp, lane);
+    producer4<kBlocks>(fp, sy, sb, sp, warp, lane);
   } else if (warp < kWarpKd4) {
     setmaxnreg_dec<kRegsMisc4>();
     if (warp == kWarpMisc4) {
@@ -767,7 +791,7 @@ __global__ void __launch_bounds__(kThreads4, 1) qsa_prefill_f4_kernel(const __gr
     v_dequant(fp, sy, sb, warp, lane);
   } else if (warp < kWarpEpi4) {
     setmaxnreg_inc<kRegsSm4>();
-    softmax4<kBlocks>(p, sy, sb, sp, tmem, warp, lane);
+    softmax4(p, sy, sb, sp, tmem, warp, lane);
   } else {
     setmaxnreg_dec<kRegsEpi4>();
     epilogue4(p, sy, sp, tmem, warp, lane);
