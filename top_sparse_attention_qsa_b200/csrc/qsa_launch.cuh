@@ -201,22 +201,43 @@ cudaError_t launch_f8(const qsa::tc::TcParams& tp, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+template <bool kBlocks, int W>
+cudaError_t launch_f4_with(const qsa::f4::F4Params& fp, int64_t units, cudaStream_t stream) {
+  static std::atomic<int> done[kMaxDevices];
+  auto kernel = qsa::f4::qsa_attn_f4_kernel<kBlocks, W>;
+  const cudaError_t e = set_smem_once(kernel, qsa::f4::H_SMEM, done);
+  if (e != cudaSuccess) return e;
+  const int nsm = sm_count();
+  if (nsm <= 0) return cudaErrorInvalidDevice;
+  kernel<<<static_cast<unsigned>(units < nsm ? units : nsm), qsa::f4::kThreads4, qsa::f4::H_SMEM, stream>>>(fp);
+  return cudaGetLastError();
+}
+
+// Warps per unit: the count whose slowest warp takes the fewest groups of 32
+// keys, counting what a unit costs beside its keys as kUnitGroups groups (Q,
+// the output, and with several warps the merge).
 template <bool kBlocks>
 cudaError_t launch_f4(const qsa::f4::F4Params& fp, cudaStream_t stream) {
-  static std::atomic<int> done[kMaxDevices];
-  static std::atomic<int> regs_ok;
-  auto kernel = qsa::f4::qsa_prefill_f4_kernel<kBlocks>;
-  using namespace qsa::f4;
-  cudaError_t e = check_register_split(
-      kernel, kThreads4,
-      128L * (kRegsProd4 + kRegsMisc4 + kRegsKd4 + kRegsVd4 + 2L * kRegsSm4 + kRegsEpi4), &regs_ok);
-  if (e != cudaSuccess) return e;
-  e = set_smem_once(kernel, qsa::f4::H_SMEM, done);
-  if (e != cudaSuccess) return e;
-  unsigned grid = 0;
-  if ((e = persistent_grid(fp.t, &grid)) != cudaSuccess) return e;
-  kernel<<<grid, qsa::f4::kThreads4, qsa::f4::H_SMEM, stream>>>(fp);
-  return cudaGetLastError();
+  const int64_t units = fp.t.T * fp.t.Hkv * fp.t.splits;
+  const int nsm = sm_count();
+  if (nsm <= 0) return cudaErrorInvalidDevice;
+  const int64_t groups = (fp.t.chunk + qsa::f4::kGroup - 1) / qsa::f4::kGroup;
+  int best = 1;
+  int64_t best_cost = 0;
+  for (int w = 1; w <= qsa::f4::kWarps4; w *= 2) {
+    const int64_t slots = static_cast<int64_t>(nsm) * (qsa::f4::kWarps4 / w);
+    const int64_t cost = ((units + slots - 1) / slots) * ((groups + w - 1) / w + (w == 1 ? 2 : 4));
+    if (w == 1 || cost < best_cost) {
+      best = w;
+      best_cost = cost;
+    }
+  }
+  switch (best) {
+    case 1: return launch_f4_with<kBlocks, 1>(fp, units, stream);
+    case 2: return launch_f4_with<kBlocks, 2>(fp, units, stream);
+    case 4: return launch_f4_with<kBlocks, 4>(fp, units, stream);
+    default: return launch_f4_with<kBlocks, 8>(fp, units, stream);
+  }
 }
 
 }  // namespace launch
