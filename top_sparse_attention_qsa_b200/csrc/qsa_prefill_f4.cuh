@@ -90,7 +90,7 @@ constexpr float kOver = tc::kRescaleLog2 + kPShift; // x above this: the running
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
       "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -115,8 +115,8 @@ __device__ __forceinline__ uint32_t lds16(uint32_t addr) {
   return v;
 }
 
-__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(addr), "r"(v) : "memory");
 }
 
 // Eight E2M1 codes (element i in bits 4i..4i+3) times the FP16 pair s: four
@@ -218,12 +218,9 @@ __device__ __forceinline__ void gather(const F4Params& fp, uint32_t dst, const c
 
 // ------------------------------------------------------------------ Q
 
-// 16-byte chunk (8 dims) c of head h sits at place c ^ swizzle in the head's
-// row: lanes of a read differ in h & 1 and in c >> 3.
-__device__ __forceinline__ uint32_t q_place(int h, int c) {
-  return h * 512 + (c & ~7) * 16 + (((c & 7) ^ ((2 * (c >> 3)) | (h & 1))) << 4);
-}
-
+// The Q tile is kept as the MMA's A fragments: step s (512 bytes), lane 4 n + j
+// (16 bytes): dims 64 j + 4 s, + 1 of heads n and n + 8, then dims + 2, + 3 of
+// the same, so that one 16-byte load is one fragment.
 // One head's row: its largest |q|, q * 2^a in FP16 with the largest in [2^14,
 // 2^15), and the score factor 2^-a * scale_log2.  Heads past the group: zeros.
 __device__ __forceinline__ void q_head(const TcParams& p, const Unit& un, uint32_t qt, float* qsc, int h, int lane) {
@@ -245,7 +242,10 @@ __device__ __forceinline__ void q_head(const TcParams& p, const Unit& un, uint32
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     o[j] = pack_f16x2(__uint_as_float(w[j] << 16) * up, __uint_as_float(w[j] & 0xffff0000u) * up);
-  sts128(qt + q_place(h, lane), o[0], o[1], o[2], o[3]);
+  // the lane's 8 dims are steps 2 (lane % 8) and + 1 of j = lane / 8
+  const uint32_t at = qt + 1024 * (lane & 7) + (4 * (h & 7) + (lane >> 3)) * 16 + (h >> 3) * 4;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) sts32(at + 512 * (j >> 1) + 8 * (j & 1), o[j]);
   if (lane == 0) qsc[h] = h < p.G ? p.scale_log2 * __int_as_float((127 - a) << 23) : 0.f;
 }
 
@@ -353,14 +353,14 @@ __global__ void __launch_bounds__(kThreads4, 1) qsa_attn_f4_kernel(const __grid_
         }
 #pragma unroll
         for (int w = 0; w < 4; ++w) {                   // 8 dims: two MMA steps
-          const uint4 qa = lds128(qt + q_place(n, 8 * j + 4 * hf + w));
-          const uint4 qb = lds128(qt + q_place(n + 8, 8 * j + 4 * hf + w));
+          const uint4 qa = lds128(qt + 1024 * (4 * hf + w) + 16 * lane);
+          const uint4 qb = lds128(qt + 1024 * (4 * hf + w) + 512 + 16 * lane);
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
             uint32_t b[4];
             dequant8(kw[t][w], w < 2 ? __low2half2(sc[t]) : __high2half2(sc[t]), b);
-            mma_f16(s[t], qa.x, qb.x, qa.y, qb.y, b[0], b[1]);
-            mma_f16(s[t], qa.z, qb.z, qa.w, qb.w, b[2], b[3]);
+            mma_f16(s[t], qa.x, qa.y, qa.z, qa.w, b[0], b[1]);
+            mma_f16(s[t], qb.x, qb.y, qb.z, qb.w, b[2], b[3]);
           }
         }
       }
@@ -369,12 +369,13 @@ __global__ void __launch_bounds__(kThreads4, 1) qsa_attn_f4_kernel(const __grid_
       float x[4][4];
       float top = -INFINITY;
       const uint32_t mine = mask >> (2 * j);
+      const bool full = mask == 0xffffffffu;
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           x[t][r] = fmaf(s[t][r], qs[r >> 1], -mx[r >> 1]);
-          if (mask != 0xffffffffu && !((mine >> (8 * t + (r & 1))) & 1u)) x[t][r] = -INFINITY;
+          if (!full) x[t][r] = (mine >> (8 * t + (r & 1))) & 1u ? x[t][r] : -INFINITY;
           top = fmaxf(top, x[t][r]);
         }
       if (__any_sync(0xffffffffu, top > kOver)) {
