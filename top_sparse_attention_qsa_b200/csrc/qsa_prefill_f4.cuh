@@ -355,13 +355,16 @@ __global__ void __launch_bounds__(kThreads4, 1) qsa_attn_f4_kernel(const __grid_
         for (int w = 0; w < 4; ++w) {                   // 8 dims: two MMA steps
           const uint4 qa = lds128(qt + 1024 * (4 * hf + w) + 16 * lane);
           const uint4 qb = lds128(qt + 1024 * (4 * hf + w) + 512 + 16 * lane);
+          // a tile's two steps are four MMAs apart: an MMA's result takes about
+          // as long, and back to back they stalled the warp
+          uint32_t b[4][4];
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            uint32_t b[4];
-            dequant8(kw[t][w], w < 2 ? __low2half2(sc[t]) : __high2half2(sc[t]), b);
-            mma_f16(s[t], qa.x, qa.y, qa.z, qa.w, b[0], b[1]);
-            mma_f16(s[t], qb.x, qb.y, qb.z, qb.w, b[2], b[3]);
-          }
+          for (int t = 0; t < 4; ++t)
+            dequant8(kw[t][w], w < 2 ? __low2half2(sc[t]) : __high2half2(sc[t]), b[t]);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) mma_f16(s[t], qa.x, qa.y, qa.z, qa.w, b[t][0], b[t][1]);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) mma_f16(s[t], qb.x, qb.y, qb.z, qb.w, b[t][2], b[t][3]);
         }
       }
 
