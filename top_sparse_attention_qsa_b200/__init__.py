@@ -20,7 +20,8 @@ _API = ("sparse_prefill_fwd", "sparse_prefill_debug_gather", "sparse_prefill_fwd
 def __getattr__(name):
     if name in _API:
         from . import _capi
-        return getattr(_capi, name)
+        value = globals()[name] = getattr(_capi, name)
+        return value
     raise AttributeError(name)
 
 

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -126,7 +127,7 @@ _lib.qsa_sparse_decode_fwd.restype = ctypes.c_int
 _lib.qsa_sparse_decode_fwd.argtypes = [ctypes.POINTER(Shape), _vp, _vp, _vp, _vp, _vp, ctypes.c_float,
                                        _vp, _vp, _vp, ctypes.c_int32, _vp, ctypes.c_size_t, _vp]
 _lib.qsa_sparse_decode_workspace_bytes.restype = ctypes.c_size_t
-_lib.qsa_sparse_decode_workspace_bytes.argtypes = [ctypes.POINTER(Shape), ctypes.c_int32]
+_lib.qsa_sparse_decode_workspace_bytes.argtypes = [_vp, ctypes.c_int32]   # a Shape, or its packed bytes
 _lib.qsa_sparse_decode_num_splits.restype = ctypes.c_int32
 _lib.qsa_sparse_decode_num_splits.argtypes = [ctypes.POINTER(Shape), ctypes.c_int32]
 _lib.qsa_sparse_decode_fwd_noalloc.restype = ctypes.c_int
@@ -150,12 +151,12 @@ _lib.qsa_indexer_scores.argtypes = [ctypes.POINTER(IndexerShape), _vp, _vp, _vp,
 _lib.qsa_indexer_fold_heads.argtypes = [ctypes.POINTER(IndexerShape), _vp, _vp, _vp]
 _lib.qsa_topk_select.argtypes = [ctypes.POINTER(IndexerShape), _vp, _vp, _vp, ctypes.c_int64, ctypes.c_int32,
                                  _vp, ctypes.c_int64, _vp, ctypes.c_int32, _vp, _vp]
-_lib.qsa_kv_append.argtypes = [ctypes.POINTER(AppendShape)] + [_vp] * 11
-_lib.qsa_kv_append_fp8.argtypes = ([ctypes.POINTER(AppendShape)] + [_vp] * 7 + [ctypes.c_float] * 2 + [_vp] * 6)
-_lib.qsa_kv_append_fp4.argtypes = ([ctypes.POINTER(AppendShape)] + [_vp] * 7 + [ctypes.c_float] * 2 + [_vp] * 8)
-_lib.qsa_sparse_prefill_fp4_fwd.argtypes = ([ctypes.POINTER(Shape), ctypes.c_int32] + [_vp] * 6 + [ctypes.c_int64] * 2
+_lib.qsa_kv_append.argtypes = [_vp] * 12
+_lib.qsa_kv_append_fp8.argtypes = [_vp] * 8 + [ctypes.c_float] * 2 + [_vp] * 6
+_lib.qsa_kv_append_fp4.argtypes = [_vp] * 8 + [ctypes.c_float] * 2 + [_vp] * 8
+_lib.qsa_sparse_prefill_fp4_fwd.argtypes = ([_vp, ctypes.c_int32] + [_vp] * 6 + [ctypes.c_int64] * 2
                                             + [_vp] * 2 + [ctypes.c_float] * 3 + [_vp] * 4)
-_lib.qsa_sparse_decode_fp4_fwd.argtypes = ([ctypes.POINTER(Shape)] + [_vp] * 5 + [ctypes.c_int64] * 2 + [_vp] * 2
+_lib.qsa_sparse_decode_fp4_fwd.argtypes = ([_vp] * 6 + [ctypes.c_int64] * 2 + [_vp] * 2
                                            + [ctypes.c_float] * 3 + [_vp] * 3
                                            + [ctypes.c_int32, _vp, ctypes.c_size_t, _vp])
 _lib.qsa_status_string.restype = ctypes.c_char_p
@@ -198,16 +199,26 @@ def _need(x: torch.Tensor, name: str, dtype, device=None, host=False):
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
 
 
-def _device_call(dev, stream, fn, *args):
-    """fn(*args, stream) with `dev` current: the library launches on the
-    current device, and a tensor's device need not be that one.  `stream`
-    None is dev's current stream."""
+def _on(x, name, dtype, d):
+    """x is a tensor of `dtype` on CUDA device number `d` (errors as _need's)."""
+    if not isinstance(x, torch.Tensor) or x.dtype is not dtype or x.get_device() != d or d < 0:
+        _need(x, name, dtype, torch.device("cuda", d) if d >= 0 else None)
+        raise ValueError(f"{name} must be a CUDA tensor")
+
+
+def _device_call(d, stream, fn, *args):
+    """fn(*args, stream) with CUDA device number `d` current: the library
+    launches on the current device, and a tensor's device need not be that
+    one.  `stream` None is the device's current stream."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev).cuda_stream
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        return _raise(fn(*args, stream))
-    with torch.cuda.device(dev):
-        return _raise(fn(*args, stream))
+        stream = torch._C._cuda_getCurrentRawStream(d)
+    if d == torch._C._cuda_getDevice():
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(d):
+            rc = fn(*args, stream)
+    if rc:
+        raise QSAError(rc)
 
 
 def make_shape(q, k_cache, topk_idx, out, lse=None) -> Shape:
@@ -724,9 +735,9 @@ class Fp4Cache:
     __slots__ = ("buffer",)
 
     def __init__(self, buffer: torch.Tensor):
-        if buffer.dtype != torch.uint8:
+        if buffer.dtype is not torch.uint8:
             raise TypeError(f"an Fp4Cache buffer must be torch.uint8, got {buffer.dtype}")
-        if buffer.dim() != 3 or buffer.shape[2] != FP4_ROW_BYTES or buffer.stride(2) != 1:
+        if buffer.dim() != 3 or buffer.size(2) != FP4_ROW_BYTES or buffer.stride(2) != 1:
             raise ValueError(f"an Fp4Cache buffer must be [S, Hkv, {FP4_ROW_BYTES}] with contiguous rows")
         self.buffer = buffer
 
@@ -761,62 +772,77 @@ def rope_table(num_positions: int, rotary_dim: int, base: float = 10000.0, devic
     return torch.cat((a.cos(), a.sin()), 1).float()
 
 
-def _append_args(k, v, positions, slots, cos_sin, caches, cache_dtype, q, q_out, interleaved, status):
-    """Checks and the shape descriptor of an append; returns (shape, q_out)."""
-    dev = k.device
-    _need(k, "k", torch.bfloat16, dev)
-    _need(v, "v", torch.bfloat16, dev)
+# The shape structs as packed bytes (native sizes and alignment, as the
+# ctypes structures above): several times cheaper to make than a Structure,
+# and the small calls are bound by what Python spends on them.
+_PACK_APPEND = struct.Struct("@q6i15q")
+_PACK_SHAPE = struct.Struct("@q4i10q")
+assert _PACK_APPEND.size == ctypes.sizeof(AppendShape) and _PACK_SHAPE.size == ctypes.sizeof(Shape)
+
+
+def _append_args(k, v, positions, slots, cos_sin, caches, cache_dtype, cache_width, q, q_out, interleaved, status):
+    """Checks of an append; returns (device number, packed shape, q_out)."""
+    d = k.get_device() if isinstance(k, torch.Tensor) else -1
+    bf16, i32 = torch.bfloat16, torch.int32
+    _on(k, "k", bf16, d)
+    _on(v, "v", bf16, d)
     if k.dim() != 3 or v.shape != k.shape:
         raise ValueError("k and v must be [T, Hkv, 256]")
     T, Hkv, Dh = k.shape
+    kst, vst = k.stride(), v.stride()
     for name, c in caches:
-        _need(c, name, cache_dtype, dev)
-        if c.dim() != 3 or c.shape[1] != Hkv:
-            raise ValueError(f"{name} must be [S, Hkv, ...] with {Hkv} KV heads")
-        if c.stride(2) != 1:
-            raise ValueError("innermost dimensions must be contiguous")
+        _on(c, name, cache_dtype, d)
     cache = caches[0][1]
-    if k.stride(2) != 1 or v.stride(2) != 1:
+    if cache.dim() != 3 or cache.size(1) != Hkv or cache.size(2) != cache_width:
+        raise ValueError(f"{caches[0][0]} must be [S, {Hkv}, {cache_width}]")
+    cst = cache.stride()
+    if kst[2] != 1 or vst[2] != 1 or cst[2] != 1:
         raise ValueError("innermost dimensions must be contiguous")
-    _need_tok(slots, "slots", T, dev)
+    _on(slots, "slots", i32, d)
+    if slots.dim() != 1 or slots.size(0) != T or (T > 1 and slots.stride(0) != 1):
+        raise ValueError("slots must be a contiguous [T] int32 tensor")
     R = P = ts = 0
     if cos_sin is not None:
-        _need(cos_sin, "cos_sin", torch.float32, dev)
-        if cos_sin.dim() != 2 or (cos_sin.shape[1] > 1 and cos_sin.stride(1) != 1):
+        _on(cos_sin, "cos_sin", torch.float32, d)
+        if cos_sin.dim() != 2 or (cos_sin.size(1) > 1 and cos_sin.stride(1) != 1):
             raise ValueError("cos_sin must be [P, R] with contiguous rows")
         P, R = cos_sin.shape
         ts = cos_sin.stride(0) if P > 1 else R
         if R > 0:
-            _need_tok(positions, "positions", T, dev)
+            _on(positions, "positions", i32, d)
+            if positions.dim() != 1 or positions.size(0) != T or (T > 1 and positions.stride(0) != 1):
+                raise ValueError("positions must be a contiguous [T] int32 tensor")
     Hq = 0
-    qs = qos = (0, 0)
+    qst = ost = (0, 0)
     if q is not None:
-        _need(q, "q", torch.bfloat16, dev)
-        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != Dh or q.stride(2) != 1:
+        _on(q, "q", bf16, d)
+        qst = q.stride()
+        if q.dim() != 3 or q.size(0) != T or q.size(2) != Dh or qst[2] != 1:
             raise ValueError("q must be [T, Hq, 256] with contiguous rows")
+        Hq = q.size(1)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
-        _need(q_out, "q_out", torch.bfloat16, dev)
-        if q_out.shape != q.shape or q_out.stride(2) != 1:
-            raise ValueError("q_out must have q's shape and contiguous rows")
-        Hq = q.shape[1]
-        qs, qos = (q.stride(0), q.stride(1)), (q_out.stride(0), q_out.stride(1))
+            q_out = q.new_empty((T, Hq, Dh))
+        else:
+            _on(q_out, "q_out", bf16, d)
+            if q_out.shape != q.shape or q_out.stride(2) != 1:
+                raise ValueError("q_out must have q's shape and contiguous rows")
+        ost = q_out.stride()
     elif q_out is not None:
         raise ValueError("q_out needs q")
     if status is not None:
-        _need(status, "status", torch.int32, dev)
-    shape = AppendShape(T, Hq, Hkv, Dh, R, 1 if interleaved else 0, 0, cache.shape[0], P, *qs, *qos,
-                        k.stride(0), k.stride(1), v.stride(0), v.stride(1), ts, cache.stride(0), cache.stride(1), 0, 0)
-    return shape, q_out
+        _on(status, "status", i32, d)
+    bs0, bs1 = (cst[0], cst[1]) if cache_dtype is torch.uint8 else (0, 0)
+    return d, _PACK_APPEND.pack(T, Hq, Hkv, Dh, R, 1 if interleaved else 0, 0, cache.size(0), P, qst[0], qst[1], ost[0],
+                                ost[1], kst[0], kst[1], vst[0], vst[1], ts, cst[0], cst[1], bs0, bs1), q_out
 
 
-def _seen_args(k, k_seen, v_seen, want_seen):
+def _seen_args(k, d, k_seen, v_seen, want_seen):
     if want_seen:
-        k_seen = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device) if k_seen is None else k_seen
-        v_seen = torch.empty(k.shape, dtype=torch.bfloat16, device=k.device) if v_seen is None else v_seen
+        k_seen = k.new_empty(k.shape) if k_seen is None else k_seen
+        v_seen = k.new_empty(k.shape) if v_seen is None else v_seen
     for name, x in (("k_seen", k_seen), ("v_seen", v_seen)):
         if x is not None:
-            _need(x, name, torch.bfloat16, k.device)
+            _on(x, name, torch.bfloat16, d)
             if x.shape != k.shape or not x.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous [T, Hkv, 256] tensor")
     return k_seen, v_seen
@@ -829,12 +855,10 @@ def kv_append(k, v, positions, slots, cos_sin, k_cache, v_cache, q=None, q_out=N
     rows `slots` (int32 [T]; negative: padding, not cached) of BF16 caches
     [S, Hkv, 256].  Returns the rotated query (q_out; q itself is allowed)."""
     _check_kv(k_cache, v_cache)
-    shape, q_out = _append_args(k, v, positions, slots, cos_sin, (("k_cache", k_cache), ("v_cache", v_cache)),
-                                torch.bfloat16, q, q_out, interleaved, status)
-    if k_cache.shape[2] != k.shape[2]:
-        raise ValueError("k_cache must be [S, Hkv, 256]")
-    _device_call(k.device, stream, _lib.qsa_kv_append, ctypes.byref(shape), _ptr(q), _ptr(q_out), _ptr(k), _ptr(v),
-                 _ptr(cos_sin), _ptr(positions), _ptr(slots), _ptr(k_cache), _ptr(v_cache), _ptr(status))
+    d, shape, q_out = _append_args(k, v, positions, slots, cos_sin, (("k_cache", k_cache), ("v_cache", v_cache)),
+                                   torch.bfloat16, HEAD_DIM, q, q_out, interleaved, status)
+    _device_call(d, stream, _lib.qsa_kv_append, shape, _ptr(q), _ptr(q_out), k.data_ptr(), v.data_ptr(), _ptr(cos_sin),
+                 _ptr(positions), slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(status))
     return q_out
 
 
@@ -845,14 +869,12 @@ def kv_append_fp8(k, v, positions, slots, cos_sin, k_cache, v_cache, k_scale: fl
     k_scale (v_scale).  Returns (q_out, k_seen, v_seen): the last two, the
     values as cached in BF16, are None unless given or asked for."""
     _check_kv(k_cache, v_cache)
-    shape, q_out = _append_args(k, v, positions, slots, cos_sin, (("k_cache", k_cache), ("v_cache", v_cache)),
-                                torch.float8_e4m3fn, q, q_out, interleaved, status)
-    if k_cache.shape[2] != k.shape[2]:
-        raise ValueError("k_cache must be [S, Hkv, 256]")
-    k_seen, v_seen = _seen_args(k, k_seen, v_seen, want_seen)
-    _device_call(k.device, stream, _lib.qsa_kv_append_fp8, ctypes.byref(shape), _ptr(q), _ptr(q_out), _ptr(k),
-                 _ptr(v), _ptr(cos_sin), _ptr(positions), _ptr(slots), float(k_scale), float(v_scale),
-                 _ptr(k_cache), _ptr(v_cache), _ptr(k_seen), _ptr(v_seen), _ptr(status))
+    d, shape, q_out = _append_args(k, v, positions, slots, cos_sin, (("k_cache", k_cache), ("v_cache", v_cache)),
+                                   torch.float8_e4m3fn, HEAD_DIM, q, q_out, interleaved, status)
+    k_seen, v_seen = _seen_args(k, d, k_seen, v_seen, want_seen)
+    _device_call(d, stream, _lib.qsa_kv_append_fp8, shape, _ptr(q), _ptr(q_out), k.data_ptr(), v.data_ptr(),
+                 _ptr(cos_sin), _ptr(positions), slots.data_ptr(), float(k_scale), float(v_scale), k_cache.data_ptr(),
+                 v_cache.data_ptr(), _ptr(k_seen), _ptr(v_seen), _ptr(status))
     return q_out, k_seen, v_seen
 
 
@@ -863,56 +885,56 @@ def kv_append_fp4(k, v, positions, slots, cos_sin, cache: Fp4Cache, k_scale: flo
     scale, about max|k| / 2688 so that the block scales use E4M3's range.
     Returns (q_out, k_seen, v_seen) as kv_append_fp8."""
     buf = cache.buffer
-    shape, q_out = _append_args(k, v, positions, slots, cos_sin, (("cache", buf),), torch.uint8, q, q_out,
-                                interleaved, status)
-    shape.bscale_stride_slot, shape.bscale_stride_head = shape.kv_stride_slot, shape.kv_stride_head
-    k_seen, v_seen = _seen_args(k, k_seen, v_seen, want_seen)
+    d, shape, q_out = _append_args(k, v, positions, slots, cos_sin, (("cache", buf),), torch.uint8, FP4_ROW_BYTES, q,
+                                   q_out, interleaved, status)
+    k_seen, v_seen = _seen_args(k, d, k_seen, v_seen, want_seen)
     b = buf.data_ptr()
-    _device_call(k.device, stream, _lib.qsa_kv_append_fp4, ctypes.byref(shape), _ptr(q), _ptr(q_out), _ptr(k),
-                 _ptr(v), _ptr(cos_sin), _ptr(positions), _ptr(slots), float(k_scale), float(v_scale), b,
-                 b + 256, b + 128, b + 272, _ptr(k_seen), _ptr(v_seen), _ptr(status))
+    _device_call(d, stream, _lib.qsa_kv_append_fp4, shape, _ptr(q), _ptr(q_out), k.data_ptr(), v.data_ptr(),
+                 _ptr(cos_sin), _ptr(positions), slots.data_ptr(), float(k_scale), float(v_scale), b, b + 256, b + 128,
+                 b + 272, _ptr(k_seen), _ptr(v_seen), _ptr(status))
     return q_out, k_seen, v_seen
 
 
 def _fp4_attention_args(q, cache: Fp4Cache, topk_idx, n_valid, out, lse, status, want_lse):
-    """Checks, outputs and the shape descriptor of an attention call over a 4-bit cache."""
-    dev = q.device
+    """Checks, outputs and the packed shape of an attention call over a 4-bit cache."""
+    d = q.get_device() if isinstance(q, torch.Tensor) else -1
     buf = cache.buffer
-    _need(q, "q", torch.bfloat16, dev)
-    _need(buf, "cache", torch.uint8, dev)
-    _need(topk_idx, "topk_idx", torch.int32, dev)
+    _on(q, "q", torch.bfloat16, d)
+    _on(buf, "cache", torch.uint8, d)
+    _on(topk_idx, "topk_idx", torch.int32, d)
     if q.dim() != 3 or topk_idx.dim() != 3:
         raise ValueError("q and topk_idx must be 3-d")
     T, Hq, Dh = q.shape
     S, Hkv, _ = buf.shape
-    K = topk_idx.shape[2]
-    if topk_idx.shape[0] != T or topk_idx.shape[1] != Hkv:
+    K = topk_idx.size(2)
+    if topk_idx.size(0) != T or topk_idx.size(1) != Hkv:
         raise ValueError("topk_idx must be [T, Hkv, K]")
     if n_valid is not None:
-        _need(n_valid, "n_valid", torch.int32, dev)
+        _on(n_valid, "n_valid", torch.int32, d)
         if not n_valid.is_contiguous() or n_valid.shape != (T, Hkv):
             raise ValueError("n_valid must be a contiguous [T, Hkv] tensor")
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        out = q.new_empty((T, Hq, Dh))
     else:
-        _need(out, "out", torch.bfloat16, dev)
+        _on(out, "out", torch.bfloat16, d)
         if out.shape != q.shape:
             raise ValueError("out must be [T, Hq, D]")
-    if q.stride(2) != 1 or out.stride(2) != 1 or (K > 1 and topk_idx.stride(2) != 1):
+    qst, ist, ost, bst = q.stride(), topk_idx.stride(), out.stride(), buf.stride()
+    if qst[2] != 1 or ost[2] != 1 or (K > 1 and ist[2] != 1):
         raise ValueError("innermost dimensions must be contiguous")
-    if lse is None:
-        if want_lse:
-            lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
-    else:
-        _need(lse, "lse", torch.float32, dev)
+    lst = Hq
+    if lse is not None:
+        _on(lse, "lse", torch.float32, d)
         if lse.shape != (T, Hq) or (Hq > 1 and lse.stride(1) != 1):
             raise ValueError("lse must be [T, Hq] with unit head stride")
+        lst = lse.stride(0)
+    elif want_lse:
+        lse = q.new_empty((T, Hq), dtype=torch.float32)
     if status is not None:
-        _need(status, "status", torch.int32, dev)
-    shape = Shape(T, Hq, Hkv, Dh, K, S, q.stride(0), q.stride(1), buf.stride(0), buf.stride(1), topk_idx.stride(0),
-                  topk_idx.stride(1), out.stride(0), out.stride(1), lse.stride(0) if lse is not None else Hq)
+        _on(status, "status", torch.int32, d)
+    shape = _PACK_SHAPE.pack(T, Hq, Hkv, Dh, K, S, qst[0], qst[1], bst[0], bst[1], ist[0], ist[1], ost[0], ost[1], lst)
     b = buf.data_ptr()
-    return shape, (b, b + 256, b + 128, b + 272, buf.stride(0), buf.stride(1)), out, lse
+    return d, shape, (b, b + 256, b + 128, b + 272, bst[0], bst[1]), out, lse
 
 
 def sparse_prefill_fp4_fwd(q, cache: Fp4Cache, topk_idx, k_scale: float, v_scale: float, n_valid=None,
@@ -921,12 +943,12 @@ def sparse_prefill_fp4_fwd(q, cache: Fp4Cache, topk_idx, k_scale: float, v_scale
     """Sparse prefill over a 4-bit cache (kv_append_fp4 writes it, with the
     same k_scale and v_scale).  Token lists (block_size 1) or microblock lists
     with an optional last_slot [T] int32.  Returns (out, lse)."""
-    shape, cargs, out, lse = _fp4_attention_args(q, cache, topk_idx, n_valid, out, lse, status, want_lse)
+    d, shape, cargs, out, lse = _fp4_attention_args(q, cache, topk_idx, n_valid, out, lse, status, want_lse)
     if last_slot is not None:
-        _need_tok(last_slot, "last_slot", q.shape[0], q.device)
-    _device_call(q.device, stream, _lib.qsa_sparse_prefill_fp4_fwd, ctypes.byref(shape), int(block_size),
-                 _ptr(last_slot), _ptr(q), *cargs, _ptr(topk_idx), _ptr(n_valid), float(scale), float(k_scale),
-                 float(v_scale), _ptr(out), _ptr(lse), _ptr(status))
+        _need_tok(last_slot, "last_slot", q.size(0), q.device)
+    _device_call(d, stream, _lib.qsa_sparse_prefill_fp4_fwd, shape, int(block_size), _ptr(last_slot), q.data_ptr(),
+                 *cargs, topk_idx.data_ptr(), _ptr(n_valid), float(scale), float(k_scale), float(v_scale),
+                 out.data_ptr(), _ptr(lse), _ptr(status))
     return out, lse
 
 
@@ -935,20 +957,29 @@ def sparse_decode_fp4_fwd(q, cache: Fp4Cache, topk_idx, k_scale: float, v_scale:
                           stream=None, want_lse: bool = True):
     """Split-K decode over a 4-bit cache.  A workspace (see
     decode_workspace_bytes) is allocated when none is given.  Returns (out, lse)."""
-    dev = q.device
-    shape, cargs, out, lse = _fp4_attention_args(q, cache, topk_idx, n_valid, out, lse, status, want_lse)
+    d, shape, cargs, out, lse = _fp4_attention_args(q, cache, topk_idx, n_valid, out, lse, status, want_lse)
+    ws = None
     ws_bytes = 0
     if workspace is None:
-        need = _lib.qsa_sparse_decode_workspace_bytes(ctypes.byref(shape), int(num_splits))
-        if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-            ws_bytes = need
+        ws_bytes = _workspace_bytes(d, shape, int(num_splits))
+        if ws_bytes > 0:
+            workspace = q.new_empty(ws_bytes, dtype=torch.uint8)
     else:
-        _need(workspace, "workspace", workspace.dtype, dev)
+        _on(workspace, "workspace", workspace.dtype, d)
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
         ws_bytes = workspace.numel() * workspace.element_size()
-    _device_call(dev, stream, _lib.qsa_sparse_decode_fp4_fwd, ctypes.byref(shape), _ptr(q), *cargs, _ptr(topk_idx),
-                 _ptr(n_valid), float(scale), float(k_scale), float(v_scale), _ptr(out), _ptr(lse), _ptr(status),
-                 int(num_splits), _ptr(workspace), ws_bytes)
+    if workspace is not None:
+        ws = workspace.data_ptr()
+    _device_call(d, stream, _lib.qsa_sparse_decode_fp4_fwd, shape, q.data_ptr(), *cargs, topk_idx.data_ptr(),
+                 _ptr(n_valid), float(scale), float(k_scale), float(v_scale), out.data_ptr(), _ptr(lse), _ptr(status),
+                 int(num_splits), ws, ws_bytes)
     return out, lse
+
+
+def _workspace_bytes(d, shape, num_splits):
+    """qsa_sparse_decode_workspace_bytes on device number `d` (its answer goes by the device's SM count)."""
+    if d == torch._C._cuda_getDevice():
+        return _lib.qsa_sparse_decode_workspace_bytes(shape, num_splits)
+    with torch.cuda.device(d):
+        return _lib.qsa_sparse_decode_workspace_bytes(shape, num_splits)
