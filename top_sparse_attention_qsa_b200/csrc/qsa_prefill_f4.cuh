@@ -221,14 +221,17 @@ __device__ __forceinline__ void gather(const F4Params& fp, uint32_t dst, const c
 // The Q tile is kept as the MMA's A fragments: step s (512 bytes), lane 4 n + j
 // (16 bytes): dims 64 j + 4 s, + 1 of heads n and n + 8, then dims + 2, + 3 of
 // the same, so that one 16-byte load is one fragment.
-// One head's row: its largest |q|, q * 2^a in FP16 with the largest in [2^14,
-// 2^15), and the score factor 2^-a * scale_log2.  Heads past the group: zeros.
-__device__ __forceinline__ void q_head(const TcParams& p, const Unit& un, uint32_t qt, float* qsc, int h, int lane) {
-  uint4 v = make_uint4(0u, 0u, 0u, 0u);
-  if (h < p.G)
-    v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q_ptr) + un.t * p.q_st +
-                                             (static_cast<int64_t>(un.g) * p.G + h) * p.q_sh) +
-              lane);
+// One head's row, 8 dims a lane (heads past the group: zeros).
+__device__ __forceinline__ uint4 q_load(const TcParams& p, const Unit& un, int h, int lane) {
+  if (h >= p.G) return make_uint4(0u, 0u, 0u, 0u);
+  return __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q_ptr) + un.t * p.q_st +
+                                              (static_cast<int64_t>(un.g) * p.G + h) * p.q_sh) +
+               lane);
+}
+
+// Its largest |q|, q * 2^a in FP16 with the largest in [2^14, 2^15), and the
+// score factor 2^-a * scale_log2.
+__device__ __forceinline__ void q_head(const TcParams& p, const uint4& v, uint32_t qt, float* qsc, int h, int lane) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t mx = 0u;
 #pragma unroll
@@ -293,12 +296,18 @@ __global__ void __launch_bounds__(kThreads4, 1) qsa_attn_f4_kernel(const __grid_
       cp_async_commit();
     };
     int32_t e_next = entry(wi);
+    uint4 qv[16 / W];                                   // every load of Q at once, behind the list's
+    if (groups > 0) {
+#pragma unroll
+      for (int h = 0; h < 16 / W; ++h) qv[h] = q_load(p, un, wi + h * W, lane);
+    }
     if (wi < groups) issue(wi, 0, e_next);
     e_next = entry(wi + W);
-
     // Q, while the first rows are on their way
-    if (groups > 0)
-      for (int h = wi; h < 16; h += W) q_head(p, un, qt, qsc, h, lane);
+    if (groups > 0) {
+#pragma unroll
+      for (int h = 0; h < 16 / W; ++h) q_head(p, qv[h], qt, qsc, wi + h * W, lane);
+    }
     sync_unit();
 
     float o[32][4];
