@@ -201,31 +201,40 @@ cudaError_t launch_f8(const qsa::tc::TcParams& tp, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-template <bool kBlocks, int W>
-cudaError_t launch_f4_with(const qsa::f4::F4Params& fp, int64_t units, cudaStream_t stream) {
-  static std::atomic<int> done[kMaxDevices];
-  auto kernel = qsa::f4::qsa_attn_f4_kernel<kBlocks, W>;
-  const cudaError_t e = set_smem_once(kernel, qsa::f4::H_SMEM, done);
+template <typename Kernel>
+cudaError_t launch_f4_kernel(Kernel kernel, int threads, int smem, std::atomic<int>* done, const qsa::f4::F4Params& fp,
+                             int64_t units, cudaStream_t stream) {
+  const cudaError_t e = set_smem_once(kernel, smem, done);
   if (e != cudaSuccess) return e;
   const int nsm = sm_count();
   if (nsm <= 0) return cudaErrorInvalidDevice;
-  kernel<<<static_cast<unsigned>(units < nsm ? units : nsm), qsa::f4::kThreads4, qsa::f4::H_SMEM, stream>>>(fp);
+  kernel<<<static_cast<unsigned>(units < nsm ? units : nsm), threads, smem, stream>>>(fp);
   return cudaGetLastError();
 }
 
+template <bool kBlocks, int W>
+cudaError_t launch_f4_with(const qsa::f4::F4Params& fp, int64_t units, cudaStream_t stream) {
+  using namespace qsa::f4;
+  static std::atomic<int> done[2][kMaxDevices];
+  if (fp.t.G <= 8)
+    return launch_f4_kernel(qsa_attn_f4_narrow_kernel<kBlocks, W>, kThreadsN, N_SMEM, done[1], fp, units, stream);
+  return launch_f4_kernel(qsa_attn_f4_kernel<kBlocks, W>, kThreads4, H_SMEM, done[0], fp, units, stream);
+}
+
 // Warps per unit: the count whose slowest warp takes the fewest groups of 32
-// keys, counting what a unit costs beside its keys as kUnitGroups groups (Q,
-// the output, and with several warps the merge).
+// keys, counting what a unit costs beside its keys as 2 groups (Q and the
+// output; 4 with the merge of several warps).
 template <bool kBlocks>
 cudaError_t launch_f4(const qsa::f4::F4Params& fp, cudaStream_t stream) {
   const int64_t units = fp.t.T * fp.t.Hkv * fp.t.splits;
   const int nsm = sm_count();
   if (nsm <= 0) return cudaErrorInvalidDevice;
+  const int warps = fp.t.G <= 8 ? qsa::f4::kWarpsN : qsa::f4::kWarps4;
   const int64_t groups = (fp.t.chunk + qsa::f4::kGroup - 1) / qsa::f4::kGroup;
   int best = 1;
   int64_t best_cost = 0;
-  for (int w = 1; w <= qsa::f4::kWarps4; w *= 2) {
-    const int64_t slots = static_cast<int64_t>(nsm) * (qsa::f4::kWarps4 / w);
+  for (int w = 1; w <= 8; w *= 2) {
+    const int64_t slots = static_cast<int64_t>(nsm) * (warps / w);
     const int64_t cost = ((units + slots - 1) / slots) * ((groups + w - 1) / w + (w == 1 ? 2 : 4));
     if (w == 1 || cost < best_cost) {
       best = w;

@@ -115,6 +115,10 @@ __device__ __forceinline__ uint32_t lds16(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
 __device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.b32 [%0], %1;\n" ::"r"(addr), "r"(v) : "memory");
 }
@@ -135,6 +139,10 @@ __device__ __forceinline__ void dequant8(uint32_t w, __half2 s, uint32_t (&out)[
     const __half2 x = __hmul2(*reinterpret_cast<__half2*>(&out[i]), s);
     out[i] = *reinterpret_cast<const uint32_t*>(&x);
   }
+}
+
+__device__ __forceinline__ uint32_t word(const uint4& v, int w) {
+  return w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w;
 }
 
 // Two E4M3 scales as FP16.
@@ -182,38 +190,52 @@ struct Walk {
 
 // ------------------------------------------------------------------ gather
 
-// One group's rows into a ring stage: lane r owns key r of the group; 8 lanes
-// per code row (four rows per instruction), then each lane its own row's
-// scales.  Masked keys (id < 0) become zeros without a read.
-__device__ __forceinline__ void gather(const F4Params& fp, uint32_t dst, const char* kc, const char* vc,
-                                       const char* kb, const char* vb, int32_t id, uint32_t mask, int lane) {
+// The K or V rows of a group: lane r holds key r's slot; 8 lanes per code row
+// (four rows per instruction), then each lane its own row's scales.  Masked
+// keys (id < 0) become zeros without a read.
+__device__ __forceinline__ void gather(uint32_t codes, uint32_t scales, const char* c0, const char* b0, int64_t c_ss,
+                                       int64_t b_ss, int32_t id, uint32_t mask, int lane) {
   const int cc = lane & 7, rsel = lane >> 3;
   // row 4 k + rsel: its swizzle phase is rsel for even k, rsel + 4 for odd k
-  const uint32_t d0 = dst + rsel * 128 + ((cc ^ rsel) << 4), d1 = dst + rsel * 128 + 512 + ((cc ^ (rsel + 4)) << 4);
+  const uint32_t d0 = codes + rsel * 128 + ((cc ^ rsel) << 4), d1 = codes + rsel * 128 + 512 + ((cc ^ (rsel + 4)) << 4);
+  c0 += cc * 16;
   if (mask == 0xffffffffu) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int64_t off = static_cast<int64_t>(__shfl_sync(0xffffffffu, id, 4 * k + rsel)) * fp.c_ss + cc * 16;
-      const uint32_t d = ((k & 1) ? d1 : d0) + (k >> 1) * 1024;
-      cp_async_16(d, kc + off, 16);
-      cp_async_16(d + kOffV, vc + off, 16);
-    }
-    const int64_t off = static_cast<int64_t>(id) * fp.b_ss;
-    cp_async_16(dst + kOffKs + lane * 16, kb + off, 16);
-    cp_async_16(dst + kOffVs + lane * 16, vb + off, 16);
+    for (int k = 0; k < 8; ++k)
+      cp_async_16(((k & 1) ? d1 : d0) + (k >> 1) * 1024,
+                  c0 + static_cast<int64_t>(__shfl_sync(0xffffffffu, id, 4 * k + rsel)) * c_ss, 16);
+    cp_async_16(scales + lane * 16, b0 + static_cast<int64_t>(id) * b_ss, 16);
   } else {
 #pragma unroll 1
     for (int k = 0; k < 8; ++k) {
       const int32_t rid = __shfl_sync(0xffffffffu, id, 4 * k + rsel);
-      const int64_t off = static_cast<int64_t>(max(rid, 0)) * fp.c_ss + cc * 16;
-      const uint32_t d = ((k & 1) ? d1 : d0) + (k >> 1) * 1024;
-      cp_async_16(d, kc + off, rid >= 0 ? 16 : 0);
-      cp_async_16(d + kOffV, vc + off, rid >= 0 ? 16 : 0);
+      cp_async_16(((k & 1) ? d1 : d0) + (k >> 1) * 1024, c0 + static_cast<int64_t>(max(rid, 0)) * c_ss,
+                  rid >= 0 ? 16 : 0);
     }
-    const int64_t off = static_cast<int64_t>(max(id, 0)) * fp.b_ss;
-    cp_async_16(dst + kOffKs + lane * 16, kb + off, id >= 0 ? 16 : 0);
-    cp_async_16(dst + kOffVs + lane * 16, vb + off, id >= 0 ? 16 : 0);
+    cp_async_16(scales + lane * 16, b0 + static_cast<int64_t>(max(id, 0)) * b_ss, id >= 0 ? 16 : 0);
   }
+}
+
+// K and V rows of a group at once (one exchange of each row's slot).
+__device__ __forceinline__ void gather_kv(const F4Params& fp, uint32_t dst, const char* kc, const char* vc,
+                                          const char* kb, const char* vb, int32_t id, uint32_t mask, int lane) {
+  if (mask != 0xffffffffu) {
+    gather(dst, dst + kOffKs, kc, kb, fp.c_ss, fp.b_ss, id, mask, lane);
+    gather(dst + kOffV, dst + kOffVs, vc, vb, fp.c_ss, fp.b_ss, id, mask, lane);
+    return;
+  }
+  const int cc = lane & 7, rsel = lane >> 3;
+  const uint32_t d0 = dst + rsel * 128 + ((cc ^ rsel) << 4), d1 = dst + rsel * 128 + 512 + ((cc ^ (rsel + 4)) << 4);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int64_t off = static_cast<int64_t>(__shfl_sync(0xffffffffu, id, 4 * k + rsel)) * fp.c_ss + cc * 16;
+    const uint32_t d = ((k & 1) ? d1 : d0) + (k >> 1) * 1024;
+    cp_async_16(d, kc + off, 16);
+    cp_async_16(d + kOffV, vc + off, 16);
+  }
+  const int64_t off = static_cast<int64_t>(id) * fp.b_ss;
+  cp_async_16(dst + kOffKs + lane * 16, kb + off, 16);
+  cp_async_16(dst + kOffVs + lane * 16, vb + off, 16);
 }
 
 // ------------------------------------------------------------------ Q
@@ -229,9 +251,8 @@ __device__ __forceinline__ uint4 q_load(const TcParams& p, const Unit& un, int h
                lane);
 }
 
-// Its largest |q|, q * 2^a in FP16 with the largest in [2^14, 2^15), and the
-// score factor 2^-a * scale_log2.
-__device__ __forceinline__ void q_head(const TcParams& p, const uint4& v, uint32_t qt, float* qsc, int h, int lane) {
+// q * 2^a in FP16 with the row's largest |q| in [2^14, 2^15); returns 2^-a.
+__device__ __forceinline__ float q_scale(const uint4& v, uint32_t (&o)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t mx = 0u;
 #pragma unroll
@@ -241,15 +262,21 @@ __device__ __forceinline__ void q_head(const TcParams& p, const uint4& v, uint32
   if (mx != 0u) a = 14 - (static_cast<int>(mx >> 23) - 127);
   a = min(a, 126);
   const float up = __int_as_float((127 + a) << 23);
-  uint32_t o[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     o[j] = pack_f16x2(__uint_as_float(w[j] << 16) * up, __uint_as_float(w[j] & 0xffff0000u) * up);
+  return __int_as_float((127 - a) << 23);
+}
+
+// A head's row into the Q tile, and its score factor 2^-a * scale_log2.
+__device__ __forceinline__ void q_head(const TcParams& p, const uint4& v, uint32_t qt, float* qsc, int h, int lane) {
+  uint32_t o[4];
+  const float down = q_scale(v, o);
   // the lane's 8 dims are steps 2 (lane % 8) and + 1 of j = lane / 8
   const uint32_t at = qt + 1024 * (lane & 7) + (4 * (h & 7) + (lane >> 3)) * 16 + (h >> 3) * 4;
 #pragma unroll
   for (int j = 0; j < 4; ++j) sts32(at + 512 * (j >> 1) + 8 * (j & 1), o[j]);
-  if (lane == 0) qsc[h] = h < p.G ? p.scale_log2 * __int_as_float((127 - a) << 23) : 0.f;
+  if (lane == 0) qsc[h] = h < p.G ? p.scale_log2 * down : 0.f;
 }
 
 // ------------------------------------------------------------------ kernel
@@ -292,7 +319,7 @@ __global__ void __launch_bounds__(kThreads4, 1) qsa_attn_f4_kernel(const __grid_
         if (p.status != nullptr) atomicOr(p.status, static_cast<int32_t>(tc::kStatusOob));
       }
       mask_next = __ballot_sync(0xffffffffu, id >= 0);
-      gather(fp, ring + stage * kStageBytes, kc, vc, kb, vb, id, mask_next, lane);
+      gather_kv(fp, ring + stage * kStageBytes, kc, vc, kb, vb, id, mask_next, lane);
       cp_async_commit();
     };
     int32_t e_next = entry(wi);
@@ -566,6 +593,357 @@ __global__ void __launch_bounds__(kThreads4, 1) qsa_attn_f4_kernel(const __grid_
         const int ch = 2 * lane + c;
         for (int w = 0; w < W; ++w) {
           const float4 v = reinterpret_cast<const float4*>(slab0 + w * kSlab + h * 256)[ch ^ (2 * (ch >> 4) + (h & 1))];
+          acc[c].x += v.x;
+          acc[c].y += v.y;
+          acc[c].z += v.z;
+          acc[c].w += v.w;
+        }
+        acc[c].x *= inv;
+        acc[c].y *= inv;
+        acc[c].z *= inv;
+        acc[c].w *= inv;
+      }
+      if (p.part_o != nullptr) {
+        float4* dst = reinterpret_cast<float4*>(p.part_o + ((row0 + h) * p.splits + un.s) * 256) + 2 * lane;
+        dst[0] = acc[0];
+        dst[1] = acc[1];
+      } else {
+        *reinterpret_cast<uint4*>(p.out + un.t * p.o_st + (static_cast<int64_t>(un.g) * p.G + h) * p.o_sh + 8 * lane) =
+            make_uint4(pack_bf16x2(acc[0].x, acc[0].y), pack_bf16x2(acc[0].z, acc[0].w),
+                       pack_bf16x2(acc[1].x, acc[1].y), pack_bf16x2(acc[1].z, acc[1].w));
+      }
+    }
+    sync_unit();                                        // slabs and Q are read before the next unit's
+  }
+}
+
+// ------------------------------------------------------------------ narrow kernel (G <= 8)
+
+// The same with the roles of rows and columns exchanged, for groups of up to
+// 8 query heads: heads are the 8 columns of the MMAs and keys (then dims) the
+// 16 rows, so that no half of an MMA goes to heads that do not exist.
+//   S^T = K Q^T   rows = keys n, n + 8 of a tile of 16, columns = heads; the same
+//                 words of K as above, two keys to a fragment
+//   O^T += V^T P^T  rows = two dims of a lane's 32, columns = heads.  P^T is
+//                 turned from "lane = key" to "lane = head" by movmatrix.
+// Half the MMAs and half the accumulators: 16 warps with 128 registers, a unit
+// each (W = 1) or W to a unit.  Each warp has one buffer for K and one for V: K
+// of the next group is asked for once the scores are done, V once the output
+// is, which with four warps to a scheduler is long before either is needed.
+constexpr int kWarpsN = 16, kThreadsN = 32 * kWarpsN;
+constexpr int kQTileN = 8 * 512;
+constexpr int N_RING = 0;
+constexpr int N_Q = N_RING + kWarpsN * kStageBytes;
+constexpr int N_QSC = N_Q + kWarpsN * kQTileN;
+constexpr int N_ML = N_QSC + kWarpsN * 8 * 4;       // per warp: mx[8], l[8] (merge)
+constexpr int N_SMEM = N_ML + kWarpsN * 16 * 4;
+static_assert(N_SMEM <= 232448, "shared memory");
+static_assert(kStageBytes >= 8 * 256 * 4, "a warp's buffer holds its output for the merge");
+
+// 8x8 transpose of 16-bit elements: lane 4 r + c holds row r, columns 2c, 2c + 1.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(v));
+  return r;
+}
+
+template <bool kBlocks, int W>
+__global__ void __launch_bounds__(kThreadsN, 1) qsa_attn_f4_narrow_kernel(const __grid_constant__ F4Params fp) {
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const TcParams& p = fp.t;
+  const uint32_t sb = smem_u32(sm);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int grp = warp / W, wi = warp % W;              // the unit slot, this warp's place in it
+  const int n = lane >> 2, j = lane & 3;
+  const uint32_t st = sb + N_RING + warp * kStageBytes;
+  const uint32_t qt = sb + N_Q + grp * kQTileN;
+  float* qsc = reinterpret_cast<float*>(sm + N_QSC) + grp * 8;
+  auto sync_unit = [&] {
+    if (W == 1)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;\n" ::"r"(1 + grp), "n"(32 * W) : "memory");
+  };
+
+  for (Walk wk(p, blockIdx.x + gridDim.x * grp, gridDim.x * (kWarpsN / W)); wk.left != 0u; wk.next()) {
+    const Unit un = wk.unit(p);
+    const int32_t* list = p.idx + un.t * p.idx_st + static_cast<int64_t>(un.g) * p.idx_sh;
+    const int32_t last = kBlocks ? last_visible(p, un.t) : 0x7fffffff;
+    const char* kc = fp.codes[0] + un.g * fp.c_sh;
+    const char* vc = fp.codes[1] + un.g * fp.c_sh;
+    const char* kb = fp.bscale[0] + un.g * fp.b_sh;
+    const char* vb = fp.bscale[1] + un.g * fp.b_sh;
+    const int groups = un.n_tiles;
+
+    auto entry = [&](int i) { return i < groups ? key_entry<kBlocks>(p, list, un, i * kGroup + lane) : -1; };
+    auto resolve = [&](int i, int32_t e) {
+      int32_t id = i < groups ? key_slot<kBlocks>(p, un, i * kGroup + lane, e, last) : -1;
+      if (id == -2) {
+        id = -1;
+        if (p.status != nullptr) atomicOr(p.status, static_cast<int32_t>(tc::kStatusOob));
+      }
+      return id;
+    };
+    // one commit per call, empty past the last group: K(0), V(0), K(1), V(1), ...
+    auto issue_k = [&](int i, int32_t id, uint32_t m) {
+      if (i < groups) gather(st, st + kOffKs, kc, kb, fp.c_ss, fp.b_ss, id, m, lane);
+      cp_async_commit();
+    };
+    auto issue_v = [&](int i, int32_t id, uint32_t m) {
+      if (i < groups) gather(st + kOffV, st + kOffVs, vc, vb, fp.c_ss, fp.b_ss, id, m, lane);
+      cp_async_commit();
+    };
+    const int32_t e_first = entry(wi);
+    uint4 qv[8 / W > 0 ? 8 / W : 1];
+    if (groups > 0) {
+#pragma unroll
+      for (int h = 0; h < (8 / W > 0 ? 8 / W : 1); ++h) qv[h] = q_load(p, un, wi + h * W, lane);
+    }
+    int32_t id = resolve(wi, e_first);
+    uint32_t mask = __ballot_sync(0xffffffffu, id >= 0);
+    issue_k(wi, id, mask);
+    issue_v(wi, id, mask);
+    int32_t e_next = entry(wi + W);
+    // Q as B fragments: 8 dims (two MMA steps) of head n, lane (n, j), per 512 bytes
+    if (groups > 0) {
+#pragma unroll
+      for (int h = 0; h < (8 / W > 0 ? 8 / W : 1); ++h) {
+        const int hd = wi + h * W;
+        uint32_t o[4];
+        const float down = q_scale(qv[h], o);
+        if (hd < 8) {
+          sts128(qt + 512 * (lane & 7) + (4 * hd + (lane >> 3)) * 16, o[0], o[1], o[2], o[3]);
+          if (lane == 0) qsc[hd] = hd < p.G ? p.scale_log2 * down : 0.f;
+        }
+      }
+    }
+    sync_unit();
+
+    float o[16][4];
+#pragma unroll
+    for (int x = 0; x < 16; ++x)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) o[x][r] = 0.f;
+    // heads 2 j and 2 j + 1 of this lane
+    float qs[2], mx[2], l[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const bool live = 2 * j + r < p.G;
+      qs[r] = live && groups > 0 ? qsc[2 * j + r] : 0.f;
+      mx[r] = live ? -INFINITY : INFINITY;
+      l[r] = 0.f;
+    }
+
+    for (int i = wi; i < groups; i += W) {
+      cp_async_wait<1>();                               // K of this group
+      __syncwarp();
+      // scores: two tiles of 16 keys; s[t] = {key n: heads 2j, 2j+1; key n + 8: the same}
+      float s[2][4];
+      uint32_t ksc[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        s[t >> 1][2 * (t & 1)] = s[t >> 1][2 * (t & 1) + 1] = 0.f;
+        ksc[t] = lds32(st + kOffKs + (8 * t + n) * 16 + 4 * j);
+      }
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {                  // 32 of the lane's 64 dims
+        uint4 kv[4];
+        __half2 sc[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          kv[t] = lds128(st + (8 * t + n) * 128 + (((2 * j + hf) ^ n) << 4));
+          sc[t] = scales2((ksc[t] >> (16 * hf)) & 0xffffu);
+        }
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {                   // 8 dims: two MMA steps
+          const uint4 q = lds128(qt + 512 * (4 * hf + w) + 16 * lane);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {                 // 16 keys
+            uint32_t b[2][4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              dequant8(word(kv[2 * t + k], w), w < 2 ? __low2half2(sc[2 * t + k]) : __high2half2(sc[2 * t + k]), b[k]);
+            mma_f16(s[t], b[0][0], b[1][0], b[0][1], b[1][1], q.x, q.y);
+            mma_f16(s[t], b[0][2], b[1][2], b[0][3], b[1][3], q.z, q.w);
+          }
+        }
+      }
+      __syncwarp();                                     // K is read
+      const uint32_t cur = mask;
+      id = resolve(i + W, e_next);
+      mask = __ballot_sync(0xffffffffu, id >= 0);
+      e_next = entry(i + 2 * W);
+      issue_k(i + W, id, mask);
+
+      float x[2][4];                                    // [t][2 k + r]: key 16 t + 8 k + n, head 2 j + r
+      float top = -INFINITY;
+      const uint32_t mine = cur >> n;
+      const bool full = cur == 0xffffffffu;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          x[t][r] = fmaf(s[t][r], qs[r & 1], -mx[r & 1]);
+          if (!full) x[t][r] = (mine >> (16 * t + 8 * (r >> 1))) & 1u ? x[t][r] : -INFINITY;
+          top = fmaxf(top, x[t][r]);
+        }
+      if (__any_sync(0xffffffffu, top > kOver)) {
+        float alpha[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float m = -INFINITY;
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              if ((mine >> (16 * t + 8 * k)) & 1u) m = fmaxf(m, s[t][2 * k + r] * qs[r]);
+#pragma unroll
+          for (int d = 4; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+          const float mn = fmaxf(mx[r], m - kPShift);
+          alpha[r] = mx[r] == mn ? 1.f : ex2(mx[r] - mn);
+          mx[r] = mn;
+          l[r] *= alpha[r];
+        }
+#pragma unroll
+        for (int y = 0; y < 16; ++y)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[y][r] *= alpha[r & 1];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            x[t][r] = (mine >> (16 * t + 8 * (r >> 1))) & 1u
+                          ? fmaf(s[t][r], qs[r & 1], -(mx[r & 1] == -INFINITY ? 0.f : mx[r & 1]))
+                          : -INFINITY;
+      }
+      uint32_t pk[2][2];                                // step t: keys 2j, 2j+1 and + 8 of head n
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          x[t][r] = ex2(x[t][r]);
+          l[r & 1] += x[t][r];
+        }
+        pk[t][0] = transpose8(pack_f16x2(x[t][0], x[t][1]));
+        pk[t][1] = transpose8(pack_f16x2(x[t][2], x[t][3]));
+      }
+      cp_async_wait<1>();                               // V of this group
+      __syncwarp();
+
+      // output: two steps of 16 keys
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint4 vw[4];                                    // keys 2j, 2j+1, 2j+8, 2j+9 of the step
+        uint32_t vs[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r7 = 2 * j + (k & 1);               // row & 7
+          const uint32_t row = 16 * u + 8 * (k >> 1) + r7;
+          vw[k] = lds128(st + kOffV + row * 128 + ((n ^ r7) << 4));
+          vs[k] = lds16(st + kOffVs + row * 16 + 2 * n);
+        }
+        const __half2 s01a = scales2(__byte_perm(vs[0], vs[1], 0x0040)), s01b = scales2(__byte_perm(vs[0], vs[1], 0x0051));
+        const __half2 s23a = scales2(__byte_perm(vs[2], vs[3], 0x0040)), s23b = scales2(__byte_perm(vs[2], vs[3], 0x0051));
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {                   // dims 8 w .. 8 w + 7 of the lane's 32
+          constexpr uint32_t M = 0x0f0f0f0fu;
+          const __half2 s01 = w < 2 ? s01a : s01b, s23 = w < 2 ? s23a : s23b;
+          const uint32_t v0 = word(vw[0], w), v1 = word(vw[1], w), v2 = word(vw[2], w), v3 = word(vw[3], w);
+          uint32_t e01[4], o01[4], e23[4], o23[4];      // even and odd dims, keys (0, 1) and (2, 3)
+          dequant8((v0 & M) | ((v1 << 4) & ~M), s01, e01);
+          dequant8(((v0 >> 4) & M) | (v1 & ~M), s01, o01);
+          dequant8((v2 & M) | ((v3 << 4) & ~M), s23, e23);
+          dequant8(((v2 >> 4) & M) | (v3 & ~M), s23, o23);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) mma_f16(o[4 * w + b], e01[b], o01[b], e23[b], o23[b], pk[u][0], pk[u][1]);
+        }
+      }
+      __syncwarp();                                     // V is read
+      issue_v(i + W, id, mask);
+    }
+    cp_async_wait<0>();
+
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int d = 4; d < 32; d *= 2) l[r] += __shfl_xor_sync(0xffffffffu, l[r], d);
+    const int64_t row0 = (un.t * p.Hkv + un.g) * p.G;
+    auto put_lse = [&](int h, float lt, float m) {
+      const float lv = lt == 0.f ? -INFINITY : (m + lg2(lt)) * 0.69314718055994531f;
+      if (p.part_lse != nullptr)
+        p.part_lse[(row0 + h) * p.splits + un.s] = lv;
+      else if (p.lse != nullptr)
+        p.lse[un.t * p.lse_st + static_cast<int64_t>(un.g) * p.G + h] = lv;
+    };
+    // head 2 j + r: dim 32 n + 2 y in o[y][r], 32 n + 2 y + 1 in o[y][2 + r]
+    if (W == 1) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int h = 2 * j + r;
+        if (h >= p.G) continue;
+        if (n == 0) put_lse(h, l[r], mx[r]);
+        const float inv = l[r] == 0.f ? 0.f : p.o_scale / l[r];
+        if (p.part_o != nullptr) {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + ((row0 + h) * p.splits + un.s) * 256 + 32 * n);
+#pragma unroll
+          for (int y = 0; y < 8; ++y)
+            dst[y] = make_float4(o[2 * y][r] * inv, o[2 * y][2 + r] * inv, o[2 * y + 1][r] * inv,
+                                 o[2 * y + 1][2 + r] * inv);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + un.t * p.o_st + (static_cast<int64_t>(un.g) * p.G + h) * p.o_sh + 32 * n);
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            dst[y] = make_uint4(pack_bf16x2(o[4 * y][r] * inv, o[4 * y][2 + r] * inv),
+                                pack_bf16x2(o[4 * y + 1][r] * inv, o[4 * y + 1][2 + r] * inv),
+                                pack_bf16x2(o[4 * y + 2][r] * inv, o[4 * y + 2][2 + r] * inv),
+                                pack_bf16x2(o[4 * y + 3][r] * inv, o[4 * y + 3][2 + r] * inv));
+        }
+      }
+      __syncwarp();                                     // Q is read before the next unit's
+      continue;
+    }
+
+    // Merge of W warps, as above
+    float* ml = reinterpret_cast<float*>(sm + N_ML) + grp * W * 16;
+    if (n == 0) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        ml[wi * 16 + 2 * j + r] = mx[r];
+        ml[wi * 16 + 8 + 2 * j + r] = l[r];
+      }
+    }
+    sync_unit();
+    float* slab0 = reinterpret_cast<float*>(sm + N_RING + grp * W * kStageBytes);
+    constexpr int kSlab = kStageBytes / 4;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int h = 2 * j + r;
+      float M = -INFINITY;
+      for (int w = 0; w < W; ++w) M = fmaxf(M, ml[w * 16 + h]);
+      const float f = mx[r] == M ? 1.f : ex2(mx[r] - M);  // a warp without a key: 0
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        // 16-byte chunk (4 dims) 8 n + y of row h, spread over the banks
+        float4* dst = reinterpret_cast<float4*>(slab0 + wi * kSlab + h * 256) + (8 * n + (y ^ (4 * (n & 1) + j)));
+        *dst = make_float4(o[2 * y][r] * f, o[2 * y][2 + r] * f, o[2 * y + 1][r] * f, o[2 * y + 1][2 + r] * f);
+      }
+    }
+    sync_unit();
+    for (int h = wi; h < p.G; h += W) {
+      float M = -INFINITY, lt = 0.f;
+      for (int w = 0; w < W; ++w) M = fmaxf(M, ml[w * 16 + h]);
+      for (int w = 0; w < W; ++w) {
+        const float m = ml[w * 16 + h];
+        lt += ml[w * 16 + 8 + h] * (m == M ? 1.f : ex2(m - M));
+      }
+      if (lane == 0) put_lse(h, lt, M);
+      const float inv = lt == 0.f ? 0.f : p.o_scale / lt;
+      float4 acc[2] = {};
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {                     // chunks 2 lane, 2 lane + 1: dims 8 lane ..
+        const int ch = 2 * lane + c, at = (ch & ~7) + ((ch & 7) ^ (4 * ((ch >> 3) & 1) + (h >> 1)));
+        for (int w = 0; w < W; ++w) {
+          const float4 v = reinterpret_cast<const float4*>(slab0 + w * kSlab + h * 256)[at];
           acc[c].x += v.x;
           acc[c].y += v.y;
           acc[c].z += v.z;
