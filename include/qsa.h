@@ -566,7 +566,8 @@ qsa_status_t qsa_kv_append_fp4(const qsa_append_shape_t* shape, const void* q,
  * same with v_scale.  shape->kv_stride_slot / kv_stride_head are the byte
  * strides of the code rows (128 bytes each), bscale_stride_* those of the
  * block scales (16 bytes each); all multiples of 16, every base 16-byte
- * aligned (QSA_ERR_ALIGN otherwise).  S < 2^31.  Token lists (block_size 1,
+ * aligned (QSA_ERR_ALIGN otherwise).  S and the slot strides are below 2^31
+ * (QSA_ERR_UNSUPPORTED otherwise).  Token lists (block_size 1,
  * last_slot NULL) or microblock lists as in qsa_sparse_prefill_block_fwd; any
  * Q layout that qsa_shape_t allows.
  *

@@ -39,6 +39,7 @@ def _decode(capi, s, ws=P, n=1 << 30, splits=2):
     (dict(num_q_heads=17), 3),
     (dict(num_slots=1 << 31), 3),
     (dict(topk=2 ** 31 - 100), 3),
+    (dict(kv_stride_slot=1 << 31), 3),
     (dict(num_tokens=-1), 2),
     (dict(kv_stride_slot=0), 2),
     (dict(kv_stride_slot=-288), 2),
@@ -60,6 +61,7 @@ def test_null_and_alignment(capi):
     assert _prefill(capi, s, ss=0) == 2
     assert _prefill(capi, s, sh=-16) == 2
     assert _prefill(capi, s, ss=296) == 4
+    assert _prefill(capi, s, ss=1 << 31) == 3
     assert _prefill(capi, s, bs=3) == 3
     assert _prefill(capi, _shape(capi, topk=1 << 28), bs=16) == 3
     assert _prefill(capi, _shape(capi, num_tokens=0), q=None, out=None) == 0

@@ -357,6 +357,8 @@ qsa_status_t run_f4(const qsa_shape_t* s, int32_t block_size, const int32_t* las
         c.bscale_stride_head % 16 != 0 || !aligned16(c.k_bscale) || !aligned16(c.v_bscale))
       return QSA_ERR_ALIGN;
   }
+  // slot strides are 32-bit in the kernels
+  if (s->kv_stride_slot > 0x7fffffffLL || c.bscale_stride_slot > 0x7fffffffLL) return QSA_ERR_UNSUPPORTED;
   if (s->num_tokens == 0) return QSA_OK;
   SplitPlan pl = {};
   if (decode && !plan_splits(s, num_splits, &pl)) return QSA_ERR_CUDA;
@@ -375,9 +377,9 @@ qsa_status_t run_f4(const qsa_shape_t* s, int32_t block_size, const int32_t* las
   fp.codes[1] = static_cast<const char*>(c.v_codes);
   fp.bscale[0] = static_cast<const char*>(c.k_bscale);
   fp.bscale[1] = static_cast<const char*>(c.v_bscale);
-  fp.c_ss = s->kv_stride_slot;
+  fp.c_ss = static_cast<int32_t>(s->kv_stride_slot);
   fp.c_sh = s->kv_stride_head;
-  fp.b_ss = c.bscale_stride_slot;
+  fp.b_ss = static_cast<int32_t>(c.bscale_stride_slot);
   fp.b_sh = c.bscale_stride_head;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (split) {

@@ -216,8 +216,9 @@ template <bool kBlocks, int W>
 cudaError_t launch_f4_with(const qsa::f4::F4Params& fp, int64_t units, cudaStream_t stream) {
   using namespace qsa::f4;
   static std::atomic<int> done[2][kMaxDevices];
-  if (fp.t.G <= 8)
-    return launch_f4_kernel(qsa_attn_f4_narrow_kernel<kBlocks, W>, kThreadsN, N_SMEM, done[1], fp, units, stream);
+  if (fp.t.G <= 8)   // (12 warps: all of them where the wide kernel has its 8)
+    return launch_f4_kernel(qsa_attn_f4_narrow_kernel<kBlocks, W == 8 ? kWarpsN : W>, kThreadsN, N_SMEM, done[1], fp,
+                            units, stream);
   return launch_f4_kernel(qsa_attn_f4_kernel<kBlocks, W>, kThreads4, H_SMEM, done[0], fp, units, stream);
 }
 
@@ -233,11 +234,12 @@ cudaError_t launch_f4(const qsa::f4::F4Params& fp, cudaStream_t stream) {
   const int64_t groups = (fp.t.chunk + qsa::f4::kGroup - 1) / qsa::f4::kGroup;
   int best = 1;
   int64_t best_cost = 0;
-  for (int w = 1; w <= 8; w *= 2) {
+  for (int w0 = 1; w0 <= 8; w0 *= 2) {
+    const int w = w0 == 8 ? warps : w0;
     const int64_t slots = static_cast<int64_t>(nsm) * (warps / w);
     const int64_t cost = ((units + slots - 1) / slots) * ((groups + w - 1) / w + (w == 1 ? 2 : 4));
     if (w == 1 || cost < best_cost) {
-      best = w;
+      best = w0;
       best_cost = cost;
     }
   }

@@ -67,7 +67,8 @@ struct F4Params {
   TcParams t;                     // its kraw / vraw / kv strides / tm_q are unused
   const char* codes[2];           // K, V
   const char* bscale[2];
-  int64_t c_ss, c_sh, b_ss, b_sh; // byte strides of the codes and of the scales
+  int64_t c_sh, b_sh;             // byte strides of the heads, codes and scales,
+  int32_t c_ss, b_ss;             // and of the slots (32 bits: one multiply-add per address)
 };
 
 constexpr int kWarps4 = 8, kThreads4 = 32 * kWarps4;
@@ -193,8 +194,8 @@ struct Walk {
 // The K or V rows of a group: lane r holds key r's slot; 8 lanes per code row
 // (four rows per instruction), then each lane its own row's scales.  Masked
 // keys (id < 0) become zeros without a read.
-__device__ __forceinline__ void gather(uint32_t codes, uint32_t scales, const char* c0, const char* b0, int64_t c_ss,
-                                       int64_t b_ss, int32_t id, uint32_t mask, int lane) {
+__device__ __forceinline__ void gather(uint32_t codes, uint32_t scales, const char* c0, const char* b0, int32_t c_ss,
+                                       int32_t b_ss, int32_t id, uint32_t mask, int lane) {
   const int cc = lane & 7, rsel = lane >> 3;
   // row 4 k + rsel: its swizzle phase is rsel for even k, rsel + 4 for odd k
   const uint32_t d0 = codes + rsel * 128 + ((cc ^ rsel) << 4), d1 = codes + rsel * 128 + 512 + ((cc ^ (rsel + 4)) << 4);
@@ -226,16 +227,17 @@ __device__ __forceinline__ void gather_kv(const F4Params& fp, uint32_t dst, cons
   }
   const int cc = lane & 7, rsel = lane >> 3;
   const uint32_t d0 = dst + rsel * 128 + ((cc ^ rsel) << 4), d1 = dst + rsel * 128 + 512 + ((cc ^ (rsel + 4)) << 4);
+  kc += cc * 16;
+  vc += cc * 16;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const int64_t off = static_cast<int64_t>(__shfl_sync(0xffffffffu, id, 4 * k + rsel)) * fp.c_ss + cc * 16;
+    const int32_t rid = __shfl_sync(0xffffffffu, id, 4 * k + rsel);
     const uint32_t d = ((k & 1) ? d1 : d0) + (k >> 1) * 1024;
-    cp_async_16(d, kc + off, 16);
-    cp_async_16(d + kOffV, vc + off, 16);
+    cp_async_16(d, kc + static_cast<int64_t>(rid) * fp.c_ss, 16);
+    cp_async_16(d + kOffV, vc + static_cast<int64_t>(rid) * fp.c_ss, 16);
   }
-  const int64_t off = static_cast<int64_t>(id) * fp.b_ss;
-  cp_async_16(dst + kOffKs + lane * 16, kb + off, 16);
-  cp_async_16(dst + kOffVs + lane * 16, vb + off, 16);
+  cp_async_16(dst + kOffKs + lane * 16, kb + static_cast<int64_t>(id) * fp.b_ss, 16);
+  cp_async_16(dst + kOffVs + lane * 16, vb + static_cast<int64_t>(id) * fp.b_ss, 16);
 }
 
 // ------------------------------------------------------------------ Q
@@ -626,11 +628,11 @@ __global__ void __launch_bounds__(kThreads4, 1) qsa_attn_f4_kernel(const __grid_
 //                 words of K as above, two keys to a fragment
 //   O^T += V^T P^T  rows = two dims of a lane's 32, columns = heads.  P^T is
 //                 turned from "lane = key" to "lane = head" by movmatrix.
-// Half the MMAs and half the accumulators: 16 warps with 128 registers, a unit
-// each (W = 1) or W to a unit.  Each warp has one buffer for K and one for V: K
+// Half the MMAs and half the accumulators: 12 warps with 168 registers, a unit
+// each (W = 1) or W to a unit (16 warps of 128 spilled and were 4 % slower).  Each warp has one buffer for K and one for V: K
 // of the next group is asked for once the scores are done, V once the output
-// is, which with four warps to a scheduler is long before either is needed.
-constexpr int kWarpsN = 16, kThreadsN = 32 * kWarpsN;
+// is, which with three warps to a scheduler is long before either is needed.
+constexpr int kWarpsN = 12, kThreadsN = 32 * kWarpsN;
 constexpr int kQTileN = 8 * 512;
 constexpr int N_RING = 0;
 constexpr int N_Q = N_RING + kWarpsN * kStageBytes;
@@ -694,10 +696,11 @@ __global__ void __launch_bounds__(kThreadsN, 1) qsa_attn_f4_narrow_kernel(const 
       cp_async_commit();
     };
     const int32_t e_first = entry(wi);
-    uint4 qv[8 / W > 0 ? 8 / W : 1];
+    constexpr int kQ = (8 + W - 1) / W;                 // heads this warp prepares
+    uint4 qv[kQ];
     if (groups > 0) {
 #pragma unroll
-      for (int h = 0; h < (8 / W > 0 ? 8 / W : 1); ++h) qv[h] = q_load(p, un, wi + h * W, lane);
+      for (int h = 0; h < kQ; ++h) qv[h] = q_load(p, un, wi + h * W, lane);
     }
     int32_t id = resolve(wi, e_first);
     uint32_t mask = __ballot_sync(0xffffffffu, id >= 0);
@@ -707,7 +710,7 @@ __global__ void __launch_bounds__(kThreadsN, 1) qsa_attn_f4_narrow_kernel(const 
     // Q as B fragments: 8 dims (two MMA steps) of head n, lane (n, j), per 512 bytes
     if (groups > 0) {
 #pragma unroll
-      for (int h = 0; h < (8 / W > 0 ? 8 / W : 1); ++h) {
+      for (int h = 0; h < kQ; ++h) {
         const int hd = wi + h * W;
         uint32_t o[4];
         const float down = q_scale(qv[h], o);
