@@ -19,10 +19,20 @@
 // wrong neighbour next to a border.  The other formats rotate in FP32 and
 // round once to the cache's type.
 //
-// One warp per row (one head of Q, K or V of one token), 8 dims per lane, so
-// that every global access is 16 bytes per lane and a row is one request; a
-// lane's rotation partners are the 16 bytes R/2 dims away, read again from
-// the row (an L1 hit).  A block scale's 16 dims belong to two adjacent lanes.
+// One warp takes kRows rows (heads of Q, K or V) of one token, 8 dims per lane,
+// so that every global access is 16 bytes per lane and a row is one request;
+// the rows of a token go round its warps, so that the few K and V rows, which
+// cost more than Q's, do not meet in one.
+// It asks for all its rows before the first use and reads the token's cosines
+// and sines once; a lane's rotation partners come from the lane that holds
+// them.  A block scale's 16 dims belong to two adjacent lanes.
+//
+// Bound by HBM: 236 MB (T = 8192, heads (24,2), BF16 cache) move in 49 us, 4.8
+// TB/s, 0.73 of the measured copy rate.  One row per warp took 90 us (a row
+// waited for its position, then its angles, then its partners, 512 bytes in
+// flight); four rows with 32 warps to the SM 57 us at 24, 49 at 32 (64
+// registers), 75 at 40 (spills).  The 4-bit append takes 61 us: its codes by
+// FP64 comparisons alone took 93.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -34,7 +44,7 @@
 namespace qsa {
 namespace ap {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4, kRows = 4;
 constexpr uint32_t kStatusOobSlot = 1u, kStatusBadPosition = 4u;
 
 enum Format { kBf16 = 0, kE4m3 = 1, kE2m1 = 2 };
@@ -73,48 +83,67 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                     pack_bf16x2(x[6], x[7]));
 }
 
-// y_a = a c - b s in FP32 (one rounding of b s, one of the difference) or in
-// FP64 (both products exact, one rounding).
-__device__ __forceinline__ float rot(float a, float c, float b, float s) { return fmaf(a, c, -__fmul_rn(b, s)); }
+// a c + b s in FP32 (one rounding of b s, one of the sum) or in FP64 (both
+// products exact, one rounding).
+__device__ __forceinline__ float rot(float a, float c, float b, float s) { return fmaf(a, c, __fmul_rn(b, s)); }
 __device__ __forceinline__ double rot(double a, double c, double b, double s) {
-  return __dsub_rn(__dmul_rn(a, c), __dmul_rn(b, s));
+  return __dadd_rn(__dmul_rn(a, c), __dmul_rn(b, s));
 }
 
-// The lane's 8 dims of a row after rotation; `row` are the row's 256 BF16.
-template <typename F>
-__device__ __forceinline__ void rotate8(const AppendParams& p, const __nv_bfloat16* row, const uint4& own,
-                                        const float* cs, int lane, F (&y)[8]) {
-  float x[8];
-  unpack8(own, x);
-  const int d0 = 8 * lane;
-  if (d0 >= p.R) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = x[i];
+// The cosines and sines of the lane's pairs: in the interleaved form of its 4
+// pairs, else of the pairs its 8 dims belong to (s negated where the lane
+// holds the pairs' first halves, so that y = x c + partner * s throughout).
+struct Angles {
+  float c[8], s[8];
+};
+
+__device__ __forceinline__ void load_angles(const AppendParams& p, int64_t pos, int lane, Angles& a) {
+  const float* cs = p.table + pos * p.table_st;
+  const int half = p.R >> 1, d0 = 8 * lane;
+  if (p.interleaved) {
+    const float4 c = __ldg(reinterpret_cast<const float4*>(cs + (d0 >> 1)));
+    const float4 s = __ldg(reinterpret_cast<const float4*>(cs + half + (d0 >> 1)));
+    a.c[0] = a.c[1] = c.x, a.c[2] = a.c[3] = c.y, a.c[4] = a.c[5] = c.z, a.c[6] = a.c[7] = c.w;
+    a.s[0] = -(a.s[1] = s.x), a.s[2] = -(a.s[3] = s.y), a.s[4] = -(a.s[5] = s.z), a.s[6] = -(a.s[7] = s.w);
     return;
   }
-  const int half = p.R >> 1;
+  const bool lo = d0 < half;
+  const int i0 = lo ? d0 : d0 - half;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const float4 c = __ldg(reinterpret_cast<const float4*>(cs + i0 + 4 * q));
+    const float4 s = __ldg(reinterpret_cast<const float4*>(cs + half + i0 + 4 * q));
+    a.c[4 * q] = c.x, a.c[4 * q + 1] = c.y, a.c[4 * q + 2] = c.z, a.c[4 * q + 3] = c.w;
+    a.s[4 * q] = lo ? -s.x : s.x, a.s[4 * q + 1] = lo ? -s.y : s.y;
+    a.s[4 * q + 2] = lo ? -s.z : s.z, a.s[4 * q + 3] = lo ? -s.w : s.w;
+  }
+}
+
+// The lane's 8 dims of a row after rotation (all 32 lanes call; lanes past the
+// rotary dims return them as they are).
+template <typename F>
+__device__ __forceinline__ void rotate8(const AppendParams& p, const uint4& own, const Angles& a, int lane, F (&y)[8]) {
+  float x[8], o[8];
+  unpack8(own, x);
   if (p.interleaved) {
-    const float4 c = *reinterpret_cast<const float4*>(cs + (d0 >> 1));
-    const float4 s = *reinterpret_cast<const float4*>(cs + half + (d0 >> 1));
-    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const F a = x[2 * i], b = x[2 * i + 1];
-      y[2 * i] = rot(a, F(cc[i]), b, F(ss[i]));
-      y[2 * i + 1] = rot(b, F(cc[i]), a, F(-ss[i]));
-    }
+    for (int i = 0; i < 8; ++i) o[i] = x[i ^ 1];
   } else {
-    const bool lo = d0 < half;
-    float o[8];
-    unpack8(*reinterpret_cast<const uint4*>(row + (lo ? d0 + half : d0 - half)), o);
-    const int i0 = lo ? d0 : d0 - half;
-    const float4 c0 = *reinterpret_cast<const float4*>(cs + i0), c1 = *reinterpret_cast<const float4*>(cs + i0 + 4);
-    const float4 s0 = *reinterpret_cast<const float4*>(cs + half + i0),
-                 s1 = *reinterpret_cast<const float4*>(cs + half + i0 + 4);
-    const float cc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-    const float ss[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+    const int step = p.R >> 4;                          // lanes between the halves
+    const int from = 8 * lane < (p.R >> 1) ? lane + step : lane - step;
+    uint4 w;
+    w.x = __shfl_sync(0xffffffffu, own.x, from & 31);
+    w.y = __shfl_sync(0xffffffffu, own.y, from & 31);
+    w.z = __shfl_sync(0xffffffffu, own.z, from & 31);
+    w.w = __shfl_sync(0xffffffffu, own.w, from & 31);
+    unpack8(w, o);
+  }
+  if (8 * lane < p.R) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = rot(F(x[i]), F(cc[i]), F(o[i]), F(lo ? ss[i] : -ss[i]));
+    for (int i = 0; i < 8; ++i) y[i] = rot(F(x[i]), F(a.c[i]), F(o[i]), F(a.s[i]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = x[i];
   }
 }
 
@@ -124,128 +153,182 @@ __device__ __forceinline__ float e4m3_value(uint32_t byte) {
   return lo;
 }
 
+// Two FP32 values -> two E2M1 codes (lo in bits 0-3), nearest, saturating at 6.
+__device__ __forceinline__ uint32_t pack_e2m1x2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b, z;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tmov.b32 %0, {b, 0, 0, 0};\n\t}\n"
+      : "=r"(r)
+      : "f"(hi), "f"(lo));
+  return r;
+}
+
 // 8 codes (element i in bits 4i .. 4i+3) and the block scale byte of the 16
-// dims of this lane and its neighbour; `val` gets code * scale (exact in FP32).
-__device__ __forceinline__ uint32_t quantise4(const double (&y)[8], float ts, float inv, uint32_t* scale_byte,
-                                              float (&val)[8]) {
-  double m = 0.0;
+// dims of this lane and its neighbour.  The quotient y / (e ts) in FP32 is
+// within 2^-22 of its value (four roundings): where codes of the quotient
+// moved by 2^-20 either way agree, they are the code; else the element lies
+// next to a border and the exact products decide.
+// f: the 8 values rounded to FP32; exact(i): |value i| in FP64.
+template <typename Exact>
+__device__ __forceinline__ uint32_t quantise4(const float (&f)[8], Exact exact, float ts, float inv,
+                                              uint32_t* scale_byte) {
+  float m = 0.f;
   bool nan = false;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    m = fmax(m, fabs(y[i]));
-    nan |= y[i] != y[i];
+    m = fmaxf(m, fabsf(f[i]));                          // (rounding keeps the order: the largest |y| rounded)
+    nan |= f[i] != f[i];
   }
-  float amax = nan ? __int_as_float(0x7fffffff) : __double2float_rn(m);
+  float amax = nan ? __int_as_float(0x7fffffff) : m;
   const float other = __shfl_xor_sync(0xffffffffu, amax, 1);
   amax = (amax != amax || other != other) ? __int_as_float(0x7fffffff) : fmaxf(amax, other);
   const uint32_t e = pack_e4m3x2(__fmul_rn(amax, inv), 0.f) & 0xffu;   // saturates at 448; NaN stays NaN
-  const float ev = e4m3_value(e);
-  const double b = static_cast<double>(ev) * static_cast<double>(ts);
-  const bool live = b > 0.0;
-  uint32_t w = 0u;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const double u = fabs(y[i]);
-    int c = 0;
-    if (live)
-      c = (u > 0.25 * b) + (u >= 0.75 * b) + (u > 1.25 * b) + (u >= 1.75 * b) + (u > 2.5 * b) + (u >= 3.5 * b) +
-          (u > 5.0 * b);
-    const bool neg = signbit(y[i]);
-    // magnitudes 0 .5 1 1.5 2 3 4 6
-    const float g = c < 4 ? 0.5f * c : (c < 6 ? c - 2.f : 2.f * c - 8.f);
-    val[i] = (neg ? -g : g) * ev;
-    w |= static_cast<uint32_t>(c | (neg ? 8 : 0)) << (4 * i);
-  }
   *scale_byte = e;
-  return w;
+  const float ev = e4m3_value(e);
+  uint32_t neg = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) neg |= (__float_as_uint(f[i]) >> 31) << (4 * i + 3);
+  if (!(ev > 0.f)) return neg;                          // zero or NaN scale: code 0
+  const float r = __frcp_rn(ev * ts);
+  uint32_t lo = 0u, hi = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float u0 = f[2 * i] * r, u1 = f[2 * i + 1] * r;
+    constexpr float kDown = 1.f - 9.5367431640625e-7f, kUp = 1.f + 9.5367431640625e-7f;   // 2^-20
+    lo |= pack_e2m1x2(u0 * kDown, u1 * kDown) << (8 * i);
+    hi |= pack_e2m1x2(u0 * kUp, u1 * kUp) << (8 * i);
+  }
+  if (lo != hi) {
+    const double b = static_cast<double>(ev) * static_cast<double>(ts);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (((lo ^ hi) >> (4 * i)) & 0xfu) {
+        const double u = exact(i);
+        const uint32_t c = (u > 0.25 * b) + (u >= 0.75 * b) + (u > 1.25 * b) + (u >= 1.75 * b) + (u > 2.5 * b) +
+                           (u >= 3.5 * b) + (u > 5.0 * b);
+        lo = (lo & ~(0xfu << (4 * i))) | (c << (4 * i));
+      }
+    }
+  }
+  return (lo & 0x77777777u) | neg;
+}
+
+// The values of 8 codes times the block scale (exact in FP32), times ts.
+__device__ __forceinline__ uint4 values4(uint32_t codes, uint32_t scale_byte, float ts) {
+  const float ev = e4m3_value(scale_byte);
+  uint32_t h[4];
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}\n"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(codes));
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f16x2_to_f32(h[i], v[2 * i], v[2 * i + 1]);
+    v[2 * i] = __fmul_rn(v[2 * i] * ev, ts);
+    v[2 * i + 1] = __fmul_rn(v[2 * i + 1] * ev, ts);
+  }
+  return pack8(v);
 }
 
 template <int kFormat>
-__global__ void __launch_bounds__(32 * kWarps) qsa_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(32 * kWarps, 8) qsa_append_kernel(const __grid_constant__ AppendParams p) {
   const int rows = p.Hq + 2 * p.Hkv;
+  const uint32_t per_tok = (rows + kRows - 1) / kRows;
   const uint32_t w = blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  const int64_t t = w / static_cast<uint32_t>(rows);
-  const int r = static_cast<int>(w - static_cast<uint32_t>(t) * rows);
+  const uint32_t tok = w / per_tok;
+  const int64_t t = tok;
+  const int r0 = static_cast<int>(w - tok * per_tok);    // rows r0, r0 + per_tok, ...
   if (t >= p.T) return;
-  const float* cs = nullptr;
+  // what depends on the token, and the warp's rows
+  const int32_t pos = p.R > 0 ? __ldg(p.positions + t) : 0;
+  const int32_t slot = __ldg(p.slots + t);
+  uint4 own[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int r = r0 + i * static_cast<int>(per_tok);
+    // plain loads: q_out may be q itself, and no lane stores before all have read
+    const __nv_bfloat16* src = r < p.Hq ? p.q + t * p.q_st + r * p.q_sh
+                               : r < p.Hq + p.Hkv ? p.k + t * p.k_st + (r - p.Hq) * p.k_sh
+                                                  : p.v + t * p.v_st + (r - p.Hq - p.Hkv) * p.v_sh;
+    if (r < rows) own[i] = *reinterpret_cast<const uint4*>(src + 8 * lane);
+  }
+  Angles an;
   if (p.R > 0) {
-    const int32_t pos = __ldg(p.positions + t);
     if (pos < 0 || pos >= p.P) {
-      if (r == 0 && lane == 0 && p.status != nullptr) atomicOr(p.status, static_cast<int32_t>(kStatusBadPosition));
+      if (r0 == 0 && lane == 0 && p.status != nullptr) atomicOr(p.status, static_cast<int32_t>(kStatusBadPosition));
       return;
     }
-    cs = p.table + pos * p.table_st;
+    if (8 * lane < p.R) load_angles(p, pos, lane, an);
   }
-  if (r < p.Hq) {
-    const __nv_bfloat16* src = p.q + t * p.q_st + r * p.q_sh;
-    __nv_bfloat16* dst = p.q_out + t * p.qo_st + r * p.qo_sh;
-    // plain loads: q_out may be q itself, and no lane stores before all have read
-    const uint4 own = *reinterpret_cast<const uint4*>(src + 8 * lane);
-    float y[8];
-    rotate8(p, src, own, cs, lane, y);
-    __syncwarp();
-    if (8 * lane < p.R || dst != src)
-      *reinterpret_cast<uint4*>(dst + 8 * lane) = 8 * lane < p.R ? pack8(y) : own;
-    return;
-  }
-  const int kv = r - p.Hq >= p.Hkv ? 1 : 0;               // K rows, then V rows
-  const int g = r - p.Hq - kv * p.Hkv;
-  const __nv_bfloat16* src = kv ? p.v + t * p.v_st + g * p.v_sh : p.k + t * p.k_st + g * p.k_sh;
-  const uint4 own = *reinterpret_cast<const uint4*>(src + 8 * lane);
-  const int32_t slot = __ldg(p.slots + t);
   const bool put = slot >= 0 && slot < p.S;
-  if (slot >= p.S && r == p.Hq && lane == 0 && p.status != nullptr)
+  if (slot >= p.S && r0 == 0 && lane == 0 && p.status != nullptr)
     atomicOr(p.status, static_cast<int32_t>(kStatusOobSlot));
-  char* row = p.cache[kv] + static_cast<int64_t>(put ? slot : 0) * p.c_ss + g * p.c_sh;
-  __nv_bfloat16* seen = p.seen[kv] == nullptr ? nullptr : p.seen[kv] + (t * p.Hkv + g) * 256 + 8 * lane;
-  if (kFormat == kE2m1) {
-    double y[8];
-    if (kv) {
-      float x[8];
-      unpack8(own, x);
+  __syncwarp();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = x[i];
+  for (int i = 0; i < kRows; ++i) {
+    const int r = r0 + i * static_cast<int>(per_tok);
+    if (r >= rows) break;
+    if (r < p.Hq) {
+      __nv_bfloat16* dst = p.q_out + t * p.qo_st + r * p.qo_sh;
+      float y[8];
+      rotate8(p, own[i], an, lane, y);
+      if (8 * lane < p.R || p.q_out != p.q)
+        *reinterpret_cast<uint4*>(dst + 8 * lane) = 8 * lane < p.R ? pack8(y) : own[i];
+      continue;
+    }
+    const int kv = r - p.Hq >= p.Hkv ? 1 : 0;             // K rows, then V rows
+    const int g = r - p.Hq - kv * p.Hkv;
+    char* row = p.cache[kv] + static_cast<int64_t>(put ? slot : 0) * p.c_ss + g * p.c_sh;
+    __nv_bfloat16* seen = p.seen[kv] == nullptr ? nullptr : p.seen[kv] + (t * p.Hkv + g) * 256 + 8 * lane;
+    if constexpr (kFormat == kE2m1) {
+      uint32_t e, codes;
+      float f[8];
+      if (kv) {
+        unpack8(own[i], f);
+        codes = quantise4(f, [&](int k) { return static_cast<double>(fabsf(f[k])); }, p.ts[1], p.inv[1], &e);
+      } else {
+        double y[8];
+        rotate8(p, own[i], an, lane, y);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = __double2float_rn(y[k]);
+        codes = quantise4(f, [&](int k) { return fabs(y[k]); }, p.ts[0], p.inv[0], &e);
+      }
+      if (put) {
+        *reinterpret_cast<uint32_t*>(row + 4 * lane) = codes;
+        if ((lane & 1) == 0)
+          p.bscale[kv][static_cast<int64_t>(slot) * p.b_ss + g * p.b_sh + (lane >> 1)] = static_cast<char>(e);
+      }
+      if (seen != nullptr) *reinterpret_cast<uint4*>(seen) = values4(codes, e, p.ts[kv]);
     } else {
-      rotate8(p, src, own, cs, lane, y);
-    }
-    uint32_t e;
-    float val[8];
-    const uint32_t codes = quantise4(y, p.ts[kv], p.inv[kv], &e, val);
-    if (put) {
-      *reinterpret_cast<uint32_t*>(row + 4 * lane) = codes;
-      if ((lane & 1) == 0)
-        p.bscale[kv][static_cast<int64_t>(slot) * p.b_ss + g * p.b_sh + (lane >> 1)] = static_cast<char>(e);
-    }
-    if (seen != nullptr) {
+      float y[8];
+      if (kv)
+        unpack8(own[i], y);
+      else
+        rotate8(p, own[i], an, lane, y);
+      if constexpr (kFormat == kBf16) {
+        if (put) *reinterpret_cast<uint4*>(row + 16 * lane) = !kv && 8 * lane < p.R ? pack8(y) : own[i];
+      } else {
+        uint32_t b[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) val[i] = __fmul_rn(val[i], p.ts[kv]);
-      *reinterpret_cast<uint4*>(seen) = pack8(val);
-    }
-    return;
-  }
-  float y[8];
-  if (kv)
-    unpack8(own, y);
-  else
-    rotate8(p, src, own, cs, lane, y);
-  if (kFormat == kBf16) {
-    if (put) *reinterpret_cast<uint4*>(row + 16 * lane) = !kv && 8 * lane < p.R ? pack8(y) : own;
-    return;
-  }
-  uint32_t b[4];
+        for (int k = 0; k < 4; ++k)
+          b[k] = pack_e4m3x2(__fdiv_rn(y[2 * k], p.ts[kv]), __fdiv_rn(y[2 * k + 1], p.ts[kv]));
+        if (put) *reinterpret_cast<uint2*>(row + 8 * lane) = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
+        if (seen != nullptr) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    b[i] = pack_e4m3x2(__fdiv_rn(y[2 * i], p.ts[kv]), __fdiv_rn(y[2 * i + 1], p.ts[kv]));
-  if (put) *reinterpret_cast<uint2*>(row + 8 * lane) = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
-  if (seen != nullptr) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f16x2_to_f32(e4m3x2_to_f16x2(b[i]), y[2 * i], y[2 * i + 1]);
-      y[2 * i] = __fmul_rn(y[2 * i], p.ts[kv]);
-      y[2 * i + 1] = __fmul_rn(y[2 * i + 1], p.ts[kv]);
+          for (int k = 0; k < 4; ++k) {
+            f16x2_to_f32(e4m3x2_to_f16x2(b[k]), y[2 * k], y[2 * k + 1]);
+            y[2 * k] = __fmul_rn(y[2 * k], p.ts[kv]);
+            y[2 * k + 1] = __fmul_rn(y[2 * k + 1], p.ts[kv]);
+          }
+          *reinterpret_cast<uint4*>(seen) = pack8(y);
+        }
+      }
     }
-    *reinterpret_cast<uint4*>(seen) = pack8(y);
   }
 }
 
