@@ -780,72 +780,85 @@ _PACK_SHAPE = struct.Struct("@q4i10q")
 assert _PACK_APPEND.size == ctypes.sizeof(AppendShape) and _PACK_SHAPE.size == ctypes.sizeof(Shape)
 
 
-def _append_args(k, v, positions, slots, cos_sin, caches, cache_dtype, cache_width, q, q_out, interleaved, status):
-    """Checks of an append; returns (device number, packed shape, q_out)."""
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+
+
+def _append_args(k, v, positions, slots, cos_sin, cache, cache_name, cache_dtype, cache_width, q, q_out, interleaved,
+                 status):
+    """Checks of an append; returns (device number, packed shape, q_out).
+    (Each test of a tensor's type and place is written out: a call apiece
+    costs as much as the rest.)"""
     d = k.get_device() if isinstance(k, torch.Tensor) else -1
-    bf16, i32 = torch.bfloat16, torch.int32
-    _on(k, "k", bf16, d)
-    _on(v, "v", bf16, d)
-    if k.dim() != 3 or v.shape != k.shape:
+    if k.dtype is not _BF16 or d < 0:
+        _on(k, "k", _BF16, d)
+    if v.dtype is not _BF16 or v.get_device() != d:
+        _on(v, "v", _BF16, d)
+    if cache.dtype is not cache_dtype or cache.get_device() != d:
+        _on(cache, cache_name, cache_dtype, d)
+    if slots.dtype is not _I32 or slots.get_device() != d:
+        _on(slots, "slots", _I32, d)
+    kshape, kst, vst, cst = k.shape, k.stride(), v.stride(), cache.stride()
+    if len(kshape) != 3 or v.shape != kshape:
         raise ValueError("k and v must be [T, Hkv, 256]")
-    T, Hkv, Dh = k.shape
-    kst, vst = k.stride(), v.stride()
-    for name, c in caches:
-        _on(c, name, cache_dtype, d)
-    cache = caches[0][1]
-    if cache.dim() != 3 or cache.size(1) != Hkv or cache.size(2) != cache_width:
-        raise ValueError(f"{caches[0][0]} must be [S, {Hkv}, {cache_width}]")
-    cst = cache.stride()
+    T, Hkv, Dh = kshape
+    cshape = cache.shape
+    if len(cshape) != 3 or cshape[1] != Hkv or cshape[2] != cache_width:
+        raise ValueError(f"{cache_name} must be [S, {Hkv}, {cache_width}]")
     if kst[2] != 1 or vst[2] != 1 or cst[2] != 1:
         raise ValueError("innermost dimensions must be contiguous")
-    _on(slots, "slots", i32, d)
-    if slots.dim() != 1 or slots.size(0) != T or (T > 1 and slots.stride(0) != 1):
+    if slots.shape != (T,) or not slots.is_contiguous():
         raise ValueError("slots must be a contiguous [T] int32 tensor")
     R = P = ts = 0
     if cos_sin is not None:
-        _on(cos_sin, "cos_sin", torch.float32, d)
-        if cos_sin.dim() != 2 or (cos_sin.size(1) > 1 and cos_sin.stride(1) != 1):
+        if cos_sin.dtype is not _F32 or cos_sin.get_device() != d:
+            _on(cos_sin, "cos_sin", _F32, d)
+        tst = cos_sin.stride()
+        if len(tst) != 2 or (tst[1] != 1 and cos_sin.size(1) > 1):
             raise ValueError("cos_sin must be [P, R] with contiguous rows")
         P, R = cos_sin.shape
-        ts = cos_sin.stride(0) if P > 1 else R
+        ts = tst[0] if P > 1 else R
         if R > 0:
-            _on(positions, "positions", i32, d)
-            if positions.dim() != 1 or positions.size(0) != T or (T > 1 and positions.stride(0) != 1):
+            if positions.dtype is not _I32 or positions.get_device() != d:
+                _on(positions, "positions", _I32, d)
+            if positions.shape != (T,) or not positions.is_contiguous():
                 raise ValueError("positions must be a contiguous [T] int32 tensor")
     Hq = 0
     qst = ost = (0, 0)
     if q is not None:
-        _on(q, "q", bf16, d)
-        qst = q.stride()
-        if q.dim() != 3 or q.size(0) != T or q.size(2) != Dh or qst[2] != 1:
+        if q.dtype is not _BF16 or q.get_device() != d:
+            _on(q, "q", _BF16, d)
+        qshape, qst = q.shape, q.stride()
+        if len(qshape) != 3 or qshape[0] != T or qshape[2] != Dh or qst[2] != 1:
             raise ValueError("q must be [T, Hq, 256] with contiguous rows")
-        Hq = q.size(1)
+        Hq = qshape[1]
         if q_out is None:
-            q_out = q.new_empty((T, Hq, Dh))
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         else:
-            _on(q_out, "q_out", bf16, d)
-            if q_out.shape != q.shape or q_out.stride(2) != 1:
+            _on(q_out, "q_out", _BF16, d)
+            if q_out.shape != qshape or q_out.stride(2) != 1:
                 raise ValueError("q_out must have q's shape and contiguous rows")
         ost = q_out.stride()
     elif q_out is not None:
         raise ValueError("q_out needs q")
     if status is not None:
-        _on(status, "status", i32, d)
-    bs0, bs1 = (cst[0], cst[1]) if cache_dtype is torch.uint8 else (0, 0)
-    return d, _PACK_APPEND.pack(T, Hq, Hkv, Dh, R, 1 if interleaved else 0, 0, cache.size(0), P, qst[0], qst[1], ost[0],
+        _on(status, "status", _I32, d)
+    bs0, bs1 = (cst[0], cst[1]) if cache_dtype is _U8 else (0, 0)
+    return d, _PACK_APPEND.pack(T, Hq, Hkv, Dh, R, 1 if interleaved else 0, 0, cshape[0], P, qst[0], qst[1], ost[0],
                                 ost[1], kst[0], kst[1], vst[0], vst[1], ts, cst[0], cst[1], bs0, bs1), q_out
 
 
 def _seen_args(k, d, k_seen, v_seen, want_seen):
-    if want_seen:
-        k_seen = k.new_empty(k.shape) if k_seen is None else k_seen
-        v_seen = k.new_empty(k.shape) if v_seen is None else v_seen
+    """The two outputs of the cached values: new ones where asked for, checked where given."""
+    out = []
     for name, x in (("k_seen", k_seen), ("v_seen", v_seen)):
-        if x is not None:
-            _on(x, name, torch.bfloat16, d)
+        if x is None:
+            x = torch.empty_like(k, memory_format=torch.contiguous_format) if want_seen else None
+        else:
+            _on(x, name, _BF16, d)
             if x.shape != k.shape or not x.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous [T, Hkv, 256] tensor")
-    return k_seen, v_seen
+        out.append(x)
+    return out
 
 
 def kv_append(k, v, positions, slots, cos_sin, k_cache, v_cache, q=None, q_out=None, interleaved: bool = False,
@@ -854,9 +867,10 @@ def kv_append(k, v, positions, slots, cos_sin, k_cache, v_cache, q=None, q_out=N
     [T, Hq, 256]) by cos_sin [P, R] at `positions` and writes k and v to the
     rows `slots` (int32 [T]; negative: padding, not cached) of BF16 caches
     [S, Hkv, 256].  Returns the rotated query (q_out; q itself is allowed)."""
+    d, shape, q_out = _append_args(k, v, positions, slots, cos_sin, k_cache, "k_cache", _BF16, HEAD_DIM, q, q_out,
+                                   interleaved, status)
+    _on(v_cache, "v_cache", _BF16, d)
     _check_kv(k_cache, v_cache)
-    d, shape, q_out = _append_args(k, v, positions, slots, cos_sin, (("k_cache", k_cache), ("v_cache", v_cache)),
-                                   torch.bfloat16, HEAD_DIM, q, q_out, interleaved, status)
     _device_call(d, stream, _lib.qsa_kv_append, shape, _ptr(q), _ptr(q_out), k.data_ptr(), v.data_ptr(), _ptr(cos_sin),
                  _ptr(positions), slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(status))
     return q_out
@@ -868,9 +882,10 @@ def kv_append_fp8(k, v, positions, slots, cos_sin, k_cache, v_cache, k_scale: fl
     """kv_append to FP8 E4M3 caches (torch.float8_e4m3fn), stored value = y /
     k_scale (v_scale).  Returns (q_out, k_seen, v_seen): the last two, the
     values as cached in BF16, are None unless given or asked for."""
+    d, shape, q_out = _append_args(k, v, positions, slots, cos_sin, k_cache, "k_cache", torch.float8_e4m3fn, HEAD_DIM,
+                                   q, q_out, interleaved, status)
+    _on(v_cache, "v_cache", torch.float8_e4m3fn, d)
     _check_kv(k_cache, v_cache)
-    d, shape, q_out = _append_args(k, v, positions, slots, cos_sin, (("k_cache", k_cache), ("v_cache", v_cache)),
-                                   torch.float8_e4m3fn, HEAD_DIM, q, q_out, interleaved, status)
     k_seen, v_seen = _seen_args(k, d, k_seen, v_seen, want_seen)
     _device_call(d, stream, _lib.qsa_kv_append_fp8, shape, _ptr(q), _ptr(q_out), k.data_ptr(), v.data_ptr(),
                  _ptr(cos_sin), _ptr(positions), slots.data_ptr(), float(k_scale), float(v_scale), k_cache.data_ptr(),
@@ -885,8 +900,8 @@ def kv_append_fp4(k, v, positions, slots, cos_sin, cache: Fp4Cache, k_scale: flo
     scale, about max|k| / 2688 so that the block scales use E4M3's range.
     Returns (q_out, k_seen, v_seen) as kv_append_fp8."""
     buf = cache.buffer
-    d, shape, q_out = _append_args(k, v, positions, slots, cos_sin, (("cache", buf),), torch.uint8, FP4_ROW_BYTES, q,
-                                   q_out, interleaved, status)
+    d, shape, q_out = _append_args(k, v, positions, slots, cos_sin, buf, "cache", _U8, FP4_ROW_BYTES, q, q_out,
+                                   interleaved, status)
     k_seen, v_seen = _seen_args(k, d, k_seen, v_seen, want_seen)
     b = buf.data_ptr()
     _device_call(d, stream, _lib.qsa_kv_append_fp4, shape, _ptr(q), _ptr(q_out), k.data_ptr(), v.data_ptr(),
@@ -899,39 +914,44 @@ def _fp4_attention_args(q, cache: Fp4Cache, topk_idx, n_valid, out, lse, status,
     """Checks, outputs and the packed shape of an attention call over a 4-bit cache."""
     d = q.get_device() if isinstance(q, torch.Tensor) else -1
     buf = cache.buffer
-    _on(q, "q", torch.bfloat16, d)
-    _on(buf, "cache", torch.uint8, d)
-    _on(topk_idx, "topk_idx", torch.int32, d)
-    if q.dim() != 3 or topk_idx.dim() != 3:
+    if q.dtype is not _BF16 or d < 0:
+        _on(q, "q", _BF16, d)
+    if buf.get_device() != d:
+        _on(buf, "cache", _U8, d)
+    if topk_idx.dtype is not _I32 or topk_idx.get_device() != d:
+        _on(topk_idx, "topk_idx", _I32, d)
+    qshape, ishape = q.shape, topk_idx.shape
+    if len(qshape) != 3 or len(ishape) != 3:
         raise ValueError("q and topk_idx must be 3-d")
-    T, Hq, Dh = q.shape
+    T, Hq, Dh = qshape
     S, Hkv, _ = buf.shape
-    K = topk_idx.size(2)
-    if topk_idx.size(0) != T or topk_idx.size(1) != Hkv:
+    K = ishape[2]
+    if ishape[0] != T or ishape[1] != Hkv:
         raise ValueError("topk_idx must be [T, Hkv, K]")
     if n_valid is not None:
-        _on(n_valid, "n_valid", torch.int32, d)
-        if not n_valid.is_contiguous() or n_valid.shape != (T, Hkv):
+        if n_valid.dtype is not _I32 or n_valid.get_device() != d:
+            _on(n_valid, "n_valid", _I32, d)
+        if n_valid.shape != (T, Hkv) or not n_valid.is_contiguous():
             raise ValueError("n_valid must be a contiguous [T, Hkv] tensor")
     if out is None:
-        out = q.new_empty((T, Hq, Dh))
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
-        _on(out, "out", torch.bfloat16, d)
-        if out.shape != q.shape:
+        _on(out, "out", _BF16, d)
+        if out.shape != qshape:
             raise ValueError("out must be [T, Hq, D]")
     qst, ist, ost, bst = q.stride(), topk_idx.stride(), out.stride(), buf.stride()
     if qst[2] != 1 or ost[2] != 1 or (K > 1 and ist[2] != 1):
         raise ValueError("innermost dimensions must be contiguous")
     lst = Hq
     if lse is not None:
-        _on(lse, "lse", torch.float32, d)
+        _on(lse, "lse", _F32, d)
         if lse.shape != (T, Hq) or (Hq > 1 and lse.stride(1) != 1):
             raise ValueError("lse must be [T, Hq] with unit head stride")
         lst = lse.stride(0)
     elif want_lse:
-        lse = q.new_empty((T, Hq), dtype=torch.float32)
+        lse = q.new_empty((T, Hq), dtype=_F32)
     if status is not None:
-        _on(status, "status", torch.int32, d)
+        _on(status, "status", _I32, d)
     shape = _PACK_SHAPE.pack(T, Hq, Hkv, Dh, K, S, qst[0], qst[1], bst[0], bst[1], ist[0], ist[1], ost[0], ost[1], lst)
     b = buf.data_ptr()
     return d, shape, (b, b + 256, b + 128, b + 272, bst[0], bst[1]), out, lse
