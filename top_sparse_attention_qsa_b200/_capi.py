@@ -8,7 +8,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 from typing import Optional
 
 import torch
@@ -22,6 +21,8 @@ if not os.path.exists(LIB_PATH):
         "(the QSA kernels have no CPU or Python fallback)")
 
 _lib = ctypes.CDLL(LIB_PATH)
+
+from . import _binding  # noqa: E402  (csrc/qsa_binding.cpp; links against libqsa.so)
 
 QSA_OK, QSA_ERR_NULL, QSA_ERR_SHAPE, QSA_ERR_UNSUPPORTED, QSA_ERR_ALIGN, QSA_ERR_CUDA, QSA_ERR_SCRATCH = range(7)
 NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -127,7 +128,7 @@ _lib.qsa_sparse_decode_fwd.restype = ctypes.c_int
 _lib.qsa_sparse_decode_fwd.argtypes = [ctypes.POINTER(Shape), _vp, _vp, _vp, _vp, _vp, ctypes.c_float,
                                        _vp, _vp, _vp, ctypes.c_int32, _vp, ctypes.c_size_t, _vp]
 _lib.qsa_sparse_decode_workspace_bytes.restype = ctypes.c_size_t
-_lib.qsa_sparse_decode_workspace_bytes.argtypes = [_vp, ctypes.c_int32]   # a Shape, or its packed bytes
+_lib.qsa_sparse_decode_workspace_bytes.argtypes = [ctypes.POINTER(Shape), ctypes.c_int32]
 _lib.qsa_sparse_decode_num_splits.restype = ctypes.c_int32
 _lib.qsa_sparse_decode_num_splits.argtypes = [ctypes.POINTER(Shape), ctypes.c_int32]
 _lib.qsa_sparse_decode_fwd_noalloc.restype = ctypes.c_int
@@ -197,28 +198,6 @@ def _need(x: torch.Tensor, name: str, dtype, device=None, host=False):
             raise ValueError(f"{name} must be a host tensor")
     elif x.device.type != "cuda" or (device is not None and x.device != device):
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
-
-
-def _on(x, name, dtype, d):
-    """x is a tensor of `dtype` on CUDA device number `d` (errors as _need's)."""
-    if not isinstance(x, torch.Tensor) or x.dtype is not dtype or x.get_device() != d or d < 0:
-        _need(x, name, dtype, torch.device("cuda", d) if d >= 0 else None)
-        raise ValueError(f"{name} must be a CUDA tensor")
-
-
-def _device_call(d, stream, fn, *args):
-    """fn(*args, stream) with CUDA device number `d` current: the library
-    launches on the current device, and a tensor's device need not be that
-    one.  `stream` None is the device's current stream."""
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(d)
-    if d == torch._C._cuda_getDevice():
-        rc = fn(*args, stream)
-    else:
-        with torch.cuda.device(d):
-            rc = fn(*args, stream)
-    if rc:
-        raise QSAError(rc)
 
 
 def make_shape(q, k_cache, topk_idx, out, lse=None) -> Shape:
@@ -772,93 +751,14 @@ def rope_table(num_positions: int, rotary_dim: int, base: float = 10000.0, devic
     return torch.cat((a.cos(), a.sin()), 1).float()
 
 
-# The shape structs as packed bytes (native sizes and alignment, as the
-# ctypes structures above): several times cheaper to make than a Structure,
-# and the small calls are bound by what Python spends on them.
-_PACK_APPEND = struct.Struct("@q6i15q")
-_PACK_SHAPE = struct.Struct("@q4i10q")
-assert _PACK_APPEND.size == ctypes.sizeof(AppendShape) and _PACK_SHAPE.size == ctypes.sizeof(Shape)
+# Checks and marshalling of these calls are in C++ (csrc/qsa_binding.cpp): a
+# kernel of theirs takes a few microseconds, and so did the same lines in
+# Python, several times over.
 
-
-_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
-
-
-def _append_args(k, v, positions, slots, cos_sin, cache, cache_name, cache_dtype, cache_width, q, q_out, interleaved,
-                 status):
-    """Checks of an append; returns (device number, packed shape, q_out).
-    (Each test of a tensor's type and place is written out: a call apiece
-    costs as much as the rest.)"""
-    d = k.get_device() if isinstance(k, torch.Tensor) else -1
-    if k.dtype is not _BF16 or d < 0:
-        _on(k, "k", _BF16, d)
-    if v.dtype is not _BF16 or v.get_device() != d:
-        _on(v, "v", _BF16, d)
-    if cache.dtype is not cache_dtype or cache.get_device() != d:
-        _on(cache, cache_name, cache_dtype, d)
-    if slots.dtype is not _I32 or slots.get_device() != d:
-        _on(slots, "slots", _I32, d)
-    kshape, kst, vst, cst = k.shape, k.stride(), v.stride(), cache.stride()
-    if len(kshape) != 3 or v.shape != kshape:
-        raise ValueError("k and v must be [T, Hkv, 256]")
-    T, Hkv, Dh = kshape
-    cshape = cache.shape
-    if len(cshape) != 3 or cshape[1] != Hkv or cshape[2] != cache_width:
-        raise ValueError(f"{cache_name} must be [S, {Hkv}, {cache_width}]")
-    if kst[2] != 1 or vst[2] != 1 or cst[2] != 1:
-        raise ValueError("innermost dimensions must be contiguous")
-    if slots.shape != (T,) or not slots.is_contiguous():
-        raise ValueError("slots must be a contiguous [T] int32 tensor")
-    R = P = ts = 0
-    if cos_sin is not None:
-        if cos_sin.dtype is not _F32 or cos_sin.get_device() != d:
-            _on(cos_sin, "cos_sin", _F32, d)
-        tst = cos_sin.stride()
-        if len(tst) != 2 or (tst[1] != 1 and cos_sin.size(1) > 1):
-            raise ValueError("cos_sin must be [P, R] with contiguous rows")
-        P, R = cos_sin.shape
-        ts = tst[0] if P > 1 else R
-        if R > 0:
-            if positions.dtype is not _I32 or positions.get_device() != d:
-                _on(positions, "positions", _I32, d)
-            if positions.shape != (T,) or not positions.is_contiguous():
-                raise ValueError("positions must be a contiguous [T] int32 tensor")
-    Hq = 0
-    qst = ost = (0, 0)
-    if q is not None:
-        if q.dtype is not _BF16 or q.get_device() != d:
-            _on(q, "q", _BF16, d)
-        qshape, qst = q.shape, q.stride()
-        if len(qshape) != 3 or qshape[0] != T or qshape[2] != Dh or qst[2] != 1:
-            raise ValueError("q must be [T, Hq, 256] with contiguous rows")
-        Hq = qshape[1]
-        if q_out is None:
-            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        else:
-            _on(q_out, "q_out", _BF16, d)
-            if q_out.shape != qshape or q_out.stride(2) != 1:
-                raise ValueError("q_out must have q's shape and contiguous rows")
-        ost = q_out.stride()
-    elif q_out is not None:
-        raise ValueError("q_out needs q")
-    if status is not None:
-        _on(status, "status", _I32, d)
-    bs0, bs1 = (cst[0], cst[1]) if cache_dtype is _U8 else (0, 0)
-    return d, _PACK_APPEND.pack(T, Hq, Hkv, Dh, R, 1 if interleaved else 0, 0, cshape[0], P, qst[0], qst[1], ost[0],
-                                ost[1], kst[0], kst[1], vst[0], vst[1], ts, cst[0], cst[1], bs0, bs1), q_out
-
-
-def _seen_args(k, d, k_seen, v_seen, want_seen):
-    """The two outputs of the cached values: new ones where asked for, checked where given."""
-    out = []
-    for name, x in (("k_seen", k_seen), ("v_seen", v_seen)):
-        if x is None:
-            x = torch.empty_like(k, memory_format=torch.contiguous_format) if want_seen else None
-        else:
-            _on(x, name, _BF16, d)
-            if x.shape != k.shape or not x.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous [T, Hkv, 256] tensor")
-        out.append(x)
-    return out
+def _outputs(r):
+    if r.__class__ is int:
+        raise QSAError(r)
+    return r
 
 
 def kv_append(k, v, positions, slots, cos_sin, k_cache, v_cache, q=None, q_out=None, interleaved: bool = False,
@@ -867,13 +767,8 @@ def kv_append(k, v, positions, slots, cos_sin, k_cache, v_cache, q=None, q_out=N
     [T, Hq, 256]) by cos_sin [P, R] at `positions` and writes k and v to the
     rows `slots` (int32 [T]; negative: padding, not cached) of BF16 caches
     [S, Hkv, 256].  Returns the rotated query (q_out; q itself is allowed)."""
-    d, shape, q_out = _append_args(k, v, positions, slots, cos_sin, k_cache, "k_cache", _BF16, HEAD_DIM, q, q_out,
-                                   interleaved, status)
-    _on(v_cache, "v_cache", _BF16, d)
-    _check_kv(k_cache, v_cache)
-    _device_call(d, stream, _lib.qsa_kv_append, shape, _ptr(q), _ptr(q_out), k.data_ptr(), v.data_ptr(), _ptr(cos_sin),
-                 _ptr(positions), slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(status))
-    return q_out
+    return _outputs(_binding.kv_append(0, k, v, positions, slots, cos_sin, k_cache, v_cache, 1.0, 1.0, q, q_out,
+                                       interleaved, None, None, False, status, stream))[0]
 
 
 def kv_append_fp8(k, v, positions, slots, cos_sin, k_cache, v_cache, k_scale: float = 1.0, v_scale: float = 1.0,
@@ -882,15 +777,8 @@ def kv_append_fp8(k, v, positions, slots, cos_sin, k_cache, v_cache, k_scale: fl
     """kv_append to FP8 E4M3 caches (torch.float8_e4m3fn), stored value = y /
     k_scale (v_scale).  Returns (q_out, k_seen, v_seen): the last two, the
     values as cached in BF16, are None unless given or asked for."""
-    d, shape, q_out = _append_args(k, v, positions, slots, cos_sin, k_cache, "k_cache", torch.float8_e4m3fn, HEAD_DIM,
-                                   q, q_out, interleaved, status)
-    _on(v_cache, "v_cache", torch.float8_e4m3fn, d)
-    _check_kv(k_cache, v_cache)
-    k_seen, v_seen = _seen_args(k, d, k_seen, v_seen, want_seen)
-    _device_call(d, stream, _lib.qsa_kv_append_fp8, shape, _ptr(q), _ptr(q_out), k.data_ptr(), v.data_ptr(),
-                 _ptr(cos_sin), _ptr(positions), slots.data_ptr(), float(k_scale), float(v_scale), k_cache.data_ptr(),
-                 v_cache.data_ptr(), _ptr(k_seen), _ptr(v_seen), _ptr(status))
-    return q_out, k_seen, v_seen
+    return _outputs(_binding.kv_append(1, k, v, positions, slots, cos_sin, k_cache, v_cache, k_scale, v_scale, q, q_out,
+                                       interleaved, k_seen, v_seen, want_seen, status, stream))
 
 
 def kv_append_fp4(k, v, positions, slots, cos_sin, cache: Fp4Cache, k_scale: float, v_scale: float, q=None,
@@ -899,62 +787,8 @@ def kv_append_fp4(k, v, positions, slots, cos_sin, cache: Fp4Cache, k_scale: flo
     """kv_append to a 4-bit cache.  k_scale (v_scale) is the tensor's FP32
     scale, about max|k| / 2688 so that the block scales use E4M3's range.
     Returns (q_out, k_seen, v_seen) as kv_append_fp8."""
-    buf = cache.buffer
-    d, shape, q_out = _append_args(k, v, positions, slots, cos_sin, buf, "cache", _U8, FP4_ROW_BYTES, q, q_out,
-                                   interleaved, status)
-    k_seen, v_seen = _seen_args(k, d, k_seen, v_seen, want_seen)
-    b = buf.data_ptr()
-    _device_call(d, stream, _lib.qsa_kv_append_fp4, shape, _ptr(q), _ptr(q_out), k.data_ptr(), v.data_ptr(),
-                 _ptr(cos_sin), _ptr(positions), slots.data_ptr(), float(k_scale), float(v_scale), b, b + 256, b + 128,
-                 b + 272, _ptr(k_seen), _ptr(v_seen), _ptr(status))
-    return q_out, k_seen, v_seen
-
-
-def _fp4_attention_args(q, cache: Fp4Cache, topk_idx, n_valid, out, lse, status, want_lse):
-    """Checks, outputs and the packed shape of an attention call over a 4-bit cache."""
-    d = q.get_device() if isinstance(q, torch.Tensor) else -1
-    buf = cache.buffer
-    if q.dtype is not _BF16 or d < 0:
-        _on(q, "q", _BF16, d)
-    if buf.get_device() != d:
-        _on(buf, "cache", _U8, d)
-    if topk_idx.dtype is not _I32 or topk_idx.get_device() != d:
-        _on(topk_idx, "topk_idx", _I32, d)
-    qshape, ishape = q.shape, topk_idx.shape
-    if len(qshape) != 3 or len(ishape) != 3:
-        raise ValueError("q and topk_idx must be 3-d")
-    T, Hq, Dh = qshape
-    S, Hkv, _ = buf.shape
-    K = ishape[2]
-    if ishape[0] != T or ishape[1] != Hkv:
-        raise ValueError("topk_idx must be [T, Hkv, K]")
-    if n_valid is not None:
-        if n_valid.dtype is not _I32 or n_valid.get_device() != d:
-            _on(n_valid, "n_valid", _I32, d)
-        if n_valid.shape != (T, Hkv) or not n_valid.is_contiguous():
-            raise ValueError("n_valid must be a contiguous [T, Hkv] tensor")
-    if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    else:
-        _on(out, "out", _BF16, d)
-        if out.shape != qshape:
-            raise ValueError("out must be [T, Hq, D]")
-    qst, ist, ost, bst = q.stride(), topk_idx.stride(), out.stride(), buf.stride()
-    if qst[2] != 1 or ost[2] != 1 or (K > 1 and ist[2] != 1):
-        raise ValueError("innermost dimensions must be contiguous")
-    lst = Hq
-    if lse is not None:
-        _on(lse, "lse", _F32, d)
-        if lse.shape != (T, Hq) or (Hq > 1 and lse.stride(1) != 1):
-            raise ValueError("lse must be [T, Hq] with unit head stride")
-        lst = lse.stride(0)
-    elif want_lse:
-        lse = q.new_empty((T, Hq), dtype=_F32)
-    if status is not None:
-        _on(status, "status", _I32, d)
-    shape = _PACK_SHAPE.pack(T, Hq, Hkv, Dh, K, S, qst[0], qst[1], bst[0], bst[1], ist[0], ist[1], ost[0], ost[1], lst)
-    b = buf.data_ptr()
-    return d, shape, (b, b + 256, b + 128, b + 272, bst[0], bst[1]), out, lse
+    return _outputs(_binding.kv_append(2, k, v, positions, slots, cos_sin, cache.buffer, None, k_scale, v_scale, q,
+                                       q_out, interleaved, k_seen, v_seen, want_seen, status, stream))
 
 
 def sparse_prefill_fp4_fwd(q, cache: Fp4Cache, topk_idx, k_scale: float, v_scale: float, n_valid=None,
@@ -963,43 +797,15 @@ def sparse_prefill_fp4_fwd(q, cache: Fp4Cache, topk_idx, k_scale: float, v_scale
     """Sparse prefill over a 4-bit cache (kv_append_fp4 writes it, with the
     same k_scale and v_scale).  Token lists (block_size 1) or microblock lists
     with an optional last_slot [T] int32.  Returns (out, lse)."""
-    d, shape, cargs, out, lse = _fp4_attention_args(q, cache, topk_idx, n_valid, out, lse, status, want_lse)
-    if last_slot is not None:
-        _need_tok(last_slot, "last_slot", q.size(0), q.device)
-    _device_call(d, stream, _lib.qsa_sparse_prefill_fp4_fwd, shape, int(block_size), _ptr(last_slot), q.data_ptr(),
-                 *cargs, topk_idx.data_ptr(), _ptr(n_valid), float(scale), float(k_scale), float(v_scale),
-                 out.data_ptr(), _ptr(lse), _ptr(status))
-    return out, lse
+    return _outputs(_binding.sparse_fp4(0, q, cache.buffer, topk_idx, k_scale, v_scale, n_valid, scale, block_size,
+                                        last_slot, 0, None, out, lse, status, stream, want_lse))
 
 
 def sparse_decode_fp4_fwd(q, cache: Fp4Cache, topk_idx, k_scale: float, v_scale: float, n_valid=None,
                           scale: float = 0.0, num_splits: int = 0, workspace=None, out=None, lse=None, status=None,
                           stream=None, want_lse: bool = True):
-    """Split-K decode over a 4-bit cache.  A workspace (see
-    decode_workspace_bytes) is allocated when none is given.  Returns (out, lse)."""
-    d, shape, cargs, out, lse = _fp4_attention_args(q, cache, topk_idx, n_valid, out, lse, status, want_lse)
-    ws = None
-    ws_bytes = 0
-    if workspace is None:
-        ws_bytes = _workspace_bytes(d, shape, int(num_splits))
-        if ws_bytes > 0:
-            workspace = q.new_empty(ws_bytes, dtype=torch.uint8)
-    else:
-        _on(workspace, "workspace", workspace.dtype, d)
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-        ws_bytes = workspace.numel() * workspace.element_size()
-    if workspace is not None:
-        ws = workspace.data_ptr()
-    _device_call(d, stream, _lib.qsa_sparse_decode_fp4_fwd, shape, q.data_ptr(), *cargs, topk_idx.data_ptr(),
-                 _ptr(n_valid), float(scale), float(k_scale), float(v_scale), out.data_ptr(), _ptr(lse), _ptr(status),
-                 int(num_splits), ws, ws_bytes)
-    return out, lse
-
-
-def _workspace_bytes(d, shape, num_splits):
-    """qsa_sparse_decode_workspace_bytes on device number `d` (its answer goes by the device's SM count)."""
-    if d == torch._C._cuda_getDevice():
-        return _lib.qsa_sparse_decode_workspace_bytes(shape, num_splits)
-    with torch.cuda.device(d):
-        return _lib.qsa_sparse_decode_workspace_bytes(shape, num_splits)
+    """Split-K decode over a 4-bit cache.  A workspace of
+    decode_workspace_bytes(q, cache.k_codes, topk_idx, num_splits) bytes is
+    allocated when none is given.  Returns (out, lse)."""
+    return _outputs(_binding.sparse_fp4(1, q, cache.buffer, topk_idx, k_scale, v_scale, n_valid, scale, 1, None,
+                                        num_splits, workspace, out, lse, status, stream, want_lse))

@@ -1,9 +1,11 @@
-"""Builds the two libraries in-tree with nvcc (sm_100a):
+"""Builds the libraries in-tree, with nvcc (sm_100a) and, for the binding, g++:
 
     libqsa.so        the kernels and the C ABI of include/qsa.h (production)
     libqsa_debug.so  measurement kernels and test hooks of include/qsa_debug.h,
                      compiled with QSA_DEBUG (the tests and the benchmark load
                      it next to libqsa.so; nothing in libqsa.so needs it)
+    _binding.so      the CPython binding of the calls whose marshalling counts
+                     (csrc/qsa_binding.cpp; against torch and libqsa.so)
 
     python -m top_sparse_attention_qsa_b200.build [--verbose]
 
@@ -17,12 +19,14 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libqsa.so")
+BINDING = os.path.join(PKG, "_binding.so")
 DEBUG_LIB = os.path.join(PKG, "libqsa_debug.so")
 DEBUG_SOURCES = ("qsa_debug_api.cu",)
 
@@ -43,7 +47,7 @@ def _sources(debug: bool = False):
 
 
 def _deps():
-    return (sorted(glob.glob(os.path.join(CSRC, "*.cu"))) + glob.glob(os.path.join(CSRC, "*.cuh"))
+    return (sorted(glob.glob(os.path.join(CSRC, "*.cu"))) + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(CSRC, "*.cuh"))
             + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)])
 
 
@@ -77,9 +81,30 @@ def _build_one(lib: str, debug: bool, force: bool, verbose: bool) -> str:
     return lib
 
 
+def _build_binding(force: bool) -> None:
+    if not force and up_to_date(BINDING) and os.path.getmtime(BINDING) >= os.path.getmtime(LIB):
+        return
+    import torch
+    base = os.path.dirname(torch.__file__)
+    lib = os.path.join(base, "lib")
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    inc = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(base, "include"),
+           os.path.join(base, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
+    cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+           + [x for i in inc for x in ("-isystem", i)] + [os.path.join(CSRC, "qsa_binding.cpp"), "-o", tmp, "-L", lib,
+           "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", "-L", PKG, "-l:libqsa.so",
+           "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib])
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = True) -> str:
-    """Builds libqsa.so and (debug=True) libqsa_debug.so; returns libqsa.so's path."""
+    """Builds libqsa.so, _binding.so and (debug=True) libqsa_debug.so; returns libqsa.so's path."""
     _build_one(LIB, False, force, verbose)
+    _build_binding(force)
     if debug:
         _build_one(DEBUG_LIB, True, force, verbose)
     return LIB

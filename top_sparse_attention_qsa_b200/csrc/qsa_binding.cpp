@@ -1,0 +1,338 @@
+// qsa_binding.cpp -- CPython binding of the cache appends and of attention
+// over a 4-bit cache.
+//
+// Argument marshalling only, as in _capi.py: tensors are checked and become
+// pointers, sizes and strides; every step of the computation runs in
+// libqsa.so's kernels.  These calls come once per layer and token, where a
+// kernel takes 3 to 10 us and the same checks in Python took 10 to 20: here
+// they take about one.
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+
+#include <ATen/ATen.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <optional>
+
+#include "qsa.h"
+
+namespace {
+
+using at::Tensor;
+
+// ---------------------------------------------------------------- arguments
+
+struct TypeFault : std::runtime_error {
+  using std::runtime_error::runtime_error;
+};
+struct ValueFault : std::runtime_error {
+  using std::runtime_error::runtime_error;
+};
+
+void need(bool ok, const char* what) {
+  if (!ok) throw ValueFault(what);
+}
+
+// A tensor of type `dt` on CUDA device `dev` (any CUDA device where dev < 0).
+const Tensor& tensor(PyObject* o, const char* name, at::ScalarType dt, int dev) {
+  if (!THPVariable_Check(o)) throw TypeFault(std::string(name) + " must be a torch.Tensor");
+  const Tensor& t = THPVariable_Unpack(o);
+  if (t.scalar_type() != dt)
+    throw TypeFault(std::string(name) + " must be " + c10::toString(dt) + ", got " + c10::toString(t.scalar_type()));
+  if (!t.is_cuda() || (dev >= 0 && t.get_device() != dev))
+    throw ValueFault(std::string(name) + " must be a CUDA tensor" + (dev >= 0 ? " on cuda:" + std::to_string(dev) : ""));
+  return t;
+}
+
+bool given(PyObject* o) { return o != Py_None; }
+
+void* ptr(PyObject* o) { return given(o) ? THPVariable_Unpack(o).data_ptr() : nullptr; }
+
+// A contiguous [n] int32 tensor.
+const int32_t* per_token(PyObject* o, const char* name, int64_t n, int dev) {
+  const Tensor& t = tensor(o, name, at::kInt, dev);
+  if (t.dim() != 1 || t.size(0) != n || !t.is_contiguous())
+    throw ValueFault(std::string(name) + " must be a contiguous [T] int32 tensor");
+  return static_cast<const int32_t*>(t.data_ptr());
+}
+
+int32_t* status_word(PyObject* o, int dev) {
+  return given(o) ? static_cast<int32_t*>(tensor(o, "status", at::kInt, dev).data_ptr()) : nullptr;
+}
+
+double number(PyObject* o) {
+  const double x = PyFloat_AsDouble(o);
+  if (x == -1.0 && PyErr_Occurred()) throw python_error();
+  return x;
+}
+
+int64_t integer(PyObject* o) {
+  const long long x = PyLong_AsLongLong(o);
+  if (x == -1 && PyErr_Occurred()) throw python_error();
+  return x;
+}
+
+void* stream_of(PyObject* o, int dev) {
+  if (given(o)) {
+    void* s = PyLong_AsVoidPtr(o);
+    if (s == nullptr && PyErr_Occurred()) throw python_error();
+    return s;
+  }
+  return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
+}
+
+// The status code, or (code 0) the outputs as a tuple.
+template <typename... T>
+PyObject* result(qsa_status_t rc, const T&... outs) {
+  if (rc != QSA_OK) return PyLong_FromLong(rc);
+  PyObject* tup = PyTuple_New(sizeof...(outs));
+  Py_ssize_t i = 0;
+  auto put = [&](const std::optional<Tensor>& t) {
+    PyObject* o;
+    if (t.has_value()) {
+      o = THPVariable_Wrap(*t);
+    } else {
+      o = Py_None;
+      Py_INCREF(o);
+    }
+    PyTuple_SET_ITEM(tup, i++, o);
+  };
+  (put(outs), ...);
+  return tup;
+}
+
+template <typename F>
+PyObject* guarded(F f) {
+  HANDLE_TH_ERRORS
+  try {
+    return f();
+  } catch (const TypeFault& e) {
+    PyErr_SetString(PyExc_TypeError, e.what());
+  } catch (const ValueFault& e) {
+    PyErr_SetString(PyExc_ValueError, e.what());
+  }
+  return nullptr;
+  END_HANDLE_TH_ERRORS
+}
+
+bool count_is(Py_ssize_t n, Py_ssize_t want) {
+  if (n == want) return true;
+  PyErr_Format(PyExc_TypeError, "expected %zd arguments, got %zd", want, n);
+  return false;
+}
+
+constexpr const char* kInner = "innermost dimensions must be contiguous";
+
+// ---------------------------------------------------------------- append
+
+// kv_append(format, k, v, positions, slots, cos_sin, k_cache, v_cache, k_scale, v_scale, q, q_out, interleaved, k_seen,
+// v_seen, want_seen, status, stream) -> status code or (q_out, k_seen, v_seen).  Formats: 0 BF16, 1 E4M3, 2 4-bit (k_cache
+// is the buffer, v_cache None).
+PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is(n, 18)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const int64_t format = integer(a[0]);
+    const auto dt = format == 0 ? at::kBFloat16 : format == 1 ? at::kFloat8_e4m3fn : at::kByte;
+    const Tensor& k = tensor(a[1], "k", at::kBFloat16, -1);
+    const int dev = k.get_device();
+    const Tensor& v = tensor(a[2], "v", at::kBFloat16, dev);
+    need(k.dim() == 3 && v.sizes() == k.sizes(), "k and v must be [T, Hkv, 256]");
+    const Tensor& kc = tensor(a[6], format == 2 ? "cache" : "k_cache", dt, dev);
+    need(kc.dim() == 3 && kc.size(1) == k.size(1) && kc.size(2) == (format == 2 ? 288 : 256),
+         format == 2 ? "cache must be [S, Hkv, 288]" : "k_cache must be [S, Hkv, 256]");
+    qsa_append_shape_t s = {};
+    s.num_tokens = k.size(0);
+    s.num_kv_heads = static_cast<int32_t>(k.size(1));
+    s.head_dim = static_cast<int32_t>(k.size(2));
+    s.num_slots = kc.size(0);
+    need(k.stride(2) == 1 && v.stride(2) == 1 && kc.stride(2) == 1, kInner);
+    if (format != 2) {
+      const Tensor& vc = tensor(a[7], "v_cache", dt, dev);
+      need(vc.sizes() == kc.sizes() && vc.strides() == kc.strides(), "k_cache and v_cache must have the same shape and strides");
+    }
+    const int32_t* slots = per_token(a[4], "slots", s.num_tokens, dev);
+    const float* table = nullptr;
+    const int32_t* positions = nullptr;
+    if (given(a[5])) {
+      const Tensor& cs = tensor(a[5], "cos_sin", at::kFloat, dev);
+      need(cs.dim() == 2 && (cs.size(1) <= 1 || cs.stride(1) == 1), "cos_sin must be [P, R] with contiguous rows");
+      need(cs.size(1) <= 256, "cos_sin has more columns than a head has dims");
+      s.num_positions = cs.size(0);
+      s.rotary_dim = static_cast<int32_t>(cs.size(1));
+      s.table_stride = cs.size(0) > 1 ? cs.stride(0) : cs.size(1);
+      table = static_cast<const float*>(cs.data_ptr());
+      if (s.rotary_dim > 0) positions = per_token(a[3], "positions", s.num_tokens, dev);
+    }
+    std::optional<Tensor> q_out;
+    if (given(a[10])) {
+      const Tensor& q = tensor(a[10], "q", at::kBFloat16, dev);
+      need(q.dim() == 3 && q.size(0) == s.num_tokens && q.size(2) == s.head_dim && q.stride(2) == 1,
+           "q must be [T, Hq, 256] with contiguous rows");
+      if (given(a[11])) {
+        q_out = tensor(a[11], "q_out", at::kBFloat16, dev);
+        need(q_out->sizes() == q.sizes() && q_out->stride(2) == 1, "q_out must have q's shape and contiguous rows");
+      } else {
+        q_out = at::empty(q.sizes(), q.options());
+      }
+      s.num_q_heads = static_cast<int32_t>(q.size(1));
+      s.q_stride_tok = q.stride(0);
+      s.q_stride_head = q.stride(1);
+      s.qo_stride_tok = q_out->stride(0);
+      s.qo_stride_head = q_out->stride(1);
+    } else {
+      need(!given(a[11]), "q_out needs q");
+    }
+    const int yes = PyObject_IsTrue(a[12]), want = PyObject_IsTrue(a[15]);
+    if (yes < 0 || want < 0) throw python_error();
+    s.interleaved = yes;
+    s.k_stride_tok = k.stride(0);
+    s.k_stride_head = k.stride(1);
+    s.v_stride_tok = v.stride(0);
+    s.v_stride_head = v.stride(1);
+    s.kv_stride_slot = kc.stride(0);
+    s.kv_stride_head = kc.stride(1);
+    std::optional<Tensor> seen[2];
+    for (int i = 0; i < 2 && format != 0; ++i) {
+      const char* name = i ? "v_seen" : "k_seen";
+      if (given(a[13 + i])) {
+        seen[i] = tensor(a[13 + i], name, at::kBFloat16, dev);
+        if (seen[i]->sizes() != k.sizes() || !seen[i]->is_contiguous())
+          throw ValueFault(std::string(name) + " must be a contiguous [T, Hkv, 256] tensor");
+      } else if (want) {
+        seen[i] = at::empty(k.sizes(), k.options());
+      }
+    }
+    int32_t* status = status_word(a[16], dev);
+    void* stream = stream_of(a[17], dev);
+    const c10::cuda::OptionalCUDAGuard on(dev == c10::cuda::current_device() ? std::nullopt
+                                                                             : std::optional<c10::Device>(k.device()));
+    void* qi = ptr(a[10]);
+    void* qo = q_out.has_value() ? q_out->data_ptr() : nullptr;
+    void* ks = seen[0].has_value() ? seen[0]->data_ptr() : nullptr;
+    void* vs = seen[1].has_value() ? seen[1]->data_ptr() : nullptr;
+    char* c = static_cast<char*>(kc.data_ptr());
+    qsa_status_t rc;
+    if (format == 0) {
+      rc = qsa_kv_append(&s, qi, qo, k.data_ptr(), v.data_ptr(), table, positions, slots, c, ptr(a[7]), status, stream);
+    } else if (format == 1) {
+      rc = qsa_kv_append_fp8(&s, qi, qo, k.data_ptr(), v.data_ptr(), table, positions, slots,
+                             static_cast<float>(number(a[8])), static_cast<float>(number(a[9])), c, ptr(a[7]), ks, vs,
+                             status, stream);
+    } else {
+      s.bscale_stride_slot = s.kv_stride_slot;
+      s.bscale_stride_head = s.kv_stride_head;
+      rc = qsa_kv_append_fp4(&s, qi, qo, k.data_ptr(), v.data_ptr(), table, positions, slots,
+                             static_cast<float>(number(a[8])), static_cast<float>(number(a[9])), c, c + 256, c + 128,
+                             c + 272, ks, vs, status, stream);
+    }
+    return result(rc, q_out, seen[0], seen[1]);
+  });
+}
+
+// ---------------------------------------------------------------- attention over a 4-bit cache
+
+// sparse_fp4(decode, q, buffer, topk_idx, k_scale, v_scale, n_valid, scale, block_size, last_slot, num_splits, workspace,
+// out, lse, status, stream, want_lse) -> status code or (out, lse)
+PyObject* sparse_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count_is(n, 17)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const bool decode = integer(a[0]) != 0;
+    const Tensor& q = tensor(a[1], "q", at::kBFloat16, -1);
+    const int dev = q.get_device();
+    const Tensor& buf = tensor(a[2], "cache", at::kByte, dev);
+    const Tensor& idx = tensor(a[3], "topk_idx", at::kInt, dev);
+    need(q.dim() == 3 && idx.dim() == 3 && buf.dim() == 3, "q, the cache and topk_idx must be 3-d");
+    qsa_shape_t s = {};
+    s.num_tokens = q.size(0);
+    s.num_q_heads = static_cast<int32_t>(q.size(1));
+    s.head_dim = static_cast<int32_t>(q.size(2));
+    s.num_slots = buf.size(0);
+    s.num_kv_heads = static_cast<int32_t>(buf.size(1));
+    need(idx.size(0) == s.num_tokens && idx.size(1) == s.num_kv_heads, "topk_idx must be [T, Hkv, K]");
+    need(idx.size(2) <= 0x7fffffff, "topk_idx has too many entries");
+    s.topk = static_cast<int32_t>(idx.size(2));
+    const int32_t* n_valid = nullptr;
+    if (given(a[6])) {
+      const Tensor& nv = tensor(a[6], "n_valid", at::kInt, dev);
+      need(nv.dim() == 2 && nv.size(0) == s.num_tokens && nv.size(1) == s.num_kv_heads && nv.is_contiguous(),
+           "n_valid must be a contiguous [T, Hkv] tensor");
+      n_valid = static_cast<const int32_t*>(nv.data_ptr());
+    }
+    const int32_t* last = given(a[9]) ? per_token(a[9], "last_slot", s.num_tokens, dev) : nullptr;
+    Tensor out;
+    if (given(a[12])) {
+      out = tensor(a[12], "out", at::kBFloat16, dev);
+      need(out.sizes() == q.sizes(), "out must be [T, Hq, D]");
+    } else {
+      out = at::empty(q.sizes(), q.options());
+    }
+    need(q.stride(2) == 1 && out.stride(2) == 1 && buf.stride(2) == 1 && (s.topk <= 1 || idx.stride(2) == 1), kInner);
+    std::optional<Tensor> lse;
+    s.lse_stride_tok = s.num_q_heads;
+    const int want = PyObject_IsTrue(a[16]);
+    if (want < 0) throw python_error();
+    if (given(a[13])) {
+      lse = tensor(a[13], "lse", at::kFloat, dev);
+      need(lse->dim() == 2 && lse->size(0) == s.num_tokens && lse->size(1) == s.num_q_heads &&
+               (s.num_q_heads <= 1 || lse->stride(1) == 1),
+           "lse must be [T, Hq] with unit head stride");
+      s.lse_stride_tok = lse->stride(0);
+    } else if (want) {
+      lse = at::empty({s.num_tokens, s.num_q_heads}, q.options().dtype(at::kFloat));
+    }
+    s.q_stride_tok = q.stride(0);
+    s.q_stride_head = q.stride(1);
+    s.kv_stride_slot = buf.stride(0);
+    s.kv_stride_head = buf.stride(1);
+    s.idx_stride_tok = idx.stride(0);
+    s.idx_stride_head = idx.stride(1);
+    s.o_stride_tok = out.stride(0);
+    s.o_stride_head = out.stride(1);
+    int32_t* status = status_word(a[14], dev);
+    void* stream = stream_of(a[15], dev);
+    const c10::cuda::OptionalCUDAGuard on(dev == c10::cuda::current_device() ? std::nullopt
+                                                                             : std::optional<c10::Device>(q.device()));
+    const char* c = static_cast<const char*>(buf.data_ptr());
+    const int32_t* list = static_cast<const int32_t*>(idx.data_ptr());
+    float* lp = lse.has_value() ? static_cast<float*>(lse->data_ptr()) : nullptr;
+    const float ks = static_cast<float>(number(a[4])), vs = static_cast<float>(number(a[5])),
+                scale = static_cast<float>(number(a[7]));
+    qsa_status_t rc;
+    if (decode) {
+      const int32_t splits = static_cast<int32_t>(integer(a[10]));
+      Tensor ws;
+      size_t bytes = 0;
+      if (given(a[11])) {
+        if (!THPVariable_Check(a[11])) throw TypeFault("workspace must be a torch.Tensor");
+        ws = THPVariable_Unpack(a[11]);
+        need(ws.is_cuda() && ws.get_device() == dev && ws.is_contiguous(), "workspace must be a contiguous CUDA tensor");
+        bytes = ws.numel() * ws.element_size();
+      } else {
+        bytes = qsa_sparse_decode_workspace_bytes(&s, splits);
+        if (bytes > 0) ws = at::empty({static_cast<int64_t>(bytes)}, buf.options());
+      }
+      rc = qsa_sparse_decode_fp4_fwd(&s, q.data_ptr(), c, c + 256, c + 128, c + 272, buf.stride(0), buf.stride(1), list,
+                                     n_valid, scale, ks, vs, out.data_ptr(), lp, status, splits,
+                                     ws.defined() ? ws.data_ptr() : nullptr, bytes, stream);
+    } else {
+      rc = qsa_sparse_prefill_fp4_fwd(&s, static_cast<int32_t>(integer(a[8])), last, q.data_ptr(), c, c + 256, c + 128,
+                                      c + 272, buf.stride(0), buf.stride(1), list, n_valid, scale, ks, vs,
+                                      out.data_ptr(), lp, status, stream);
+    }
+    return result(rc, std::optional<Tensor>(out), lse);
+  });
+}
+
+PyMethodDef kMethods[] = {
+    {"kv_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_append)), METH_FASTCALL, nullptr},
+    {"sparse_fp4", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(sparse_fp4)), METH_FASTCALL, nullptr},
+    {nullptr, nullptr, 0, nullptr}};
+
+PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&kModule); }
