@@ -174,18 +174,25 @@ struct Walk {
       ++g;
     }
   }
+  // The unit's place; n_eff and n_tiles as if the whole list counted.
   __device__ Unit unit(const TcParams& p) const {
     Unit r;
     const uint32_t t = p.splits == 1 ? rem : rem / static_cast<uint32_t>(p.splits);
     r.g = static_cast<int>(g);
     r.t = t;
     r.s = static_cast<int>(rem - t * p.splits);
-    int n = p.K;
-    if (p.n_valid != nullptr) n = min(n, max(__ldg(p.n_valid + r.t * p.Hkv + r.g), 0));
     r.j0 = r.s * p.chunk;
-    r.n_eff = max(0, min((n << p.block_shift) - r.j0, p.chunk));
+    r.n_eff = max(0, min((p.K << p.block_shift) - r.j0, p.chunk));
     r.n_tiles = (r.n_eff + kGroup - 1) / kGroup;     // groups of 32 keys
     return r;
+  }
+  // Cuts the unit to n_valid entries.  The first entries are asked for before
+  // this, so that the two loads do not wait for one another.
+  __device__ static void cut(const TcParams& p, Unit& r) {
+    if (p.n_valid == nullptr) return;
+    const int n = min(p.K, max(__ldg(p.n_valid + r.t * p.Hkv + r.g), 0));
+    r.n_eff = max(0, min((n << p.block_shift) - r.j0, p.chunk));
+    r.n_tiles = (r.n_eff + kGroup - 1) / kGroup;
   }
 };
 
@@ -302,8 +309,11 @@ __global__ void __launch_bounds__(kThreads4, 1) qsa_attn_f4_kernel(const __grid_
   };
 
   for (Walk wk(p, blockIdx.x + gridDim.x * grp, gridDim.x * (kWarps4 / W)); wk.left != 0u; wk.next()) {
-    const Unit un = wk.unit(p);
+    Unit un = wk.unit(p);
     const int32_t* list = p.idx + un.t * p.idx_st + static_cast<int64_t>(un.g) * p.idx_sh;
+    const int32_t e_ask = key_entry<kBlocks>(p, list, un, wi * kGroup + lane);
+    Walk::cut(p, un);
+    const int32_t e_first = wi * kGroup + lane < un.n_eff ? e_ask : -1;
     const int32_t last = kBlocks ? last_visible(p, un.t) : 0x7fffffff;
     const char* kc = fp.codes[0] + un.g * fp.c_sh;
     const char* vc = fp.codes[1] + un.g * fp.c_sh;
@@ -324,7 +334,7 @@ __global__ void __launch_bounds__(kThreads4, 1) qsa_attn_f4_kernel(const __grid_
       gather_kv(fp, ring + stage * kStageBytes, kc, vc, kb, vb, id, mask_next, lane);
       cp_async_commit();
     };
-    int32_t e_next = entry(wi);
+    int32_t e_next = e_first;
     uint4 qv[16 / W];                                   // every load of Q at once, behind the list's
     if (groups > 0) {
 #pragma unroll
@@ -668,8 +678,11 @@ __global__ void __launch_bounds__(kThreadsN, 1) qsa_attn_f4_narrow_kernel(const 
   };
 
   for (Walk wk(p, blockIdx.x + gridDim.x * grp, gridDim.x * (kWarpsN / W)); wk.left != 0u; wk.next()) {
-    const Unit un = wk.unit(p);
+    Unit un = wk.unit(p);
     const int32_t* list = p.idx + un.t * p.idx_st + static_cast<int64_t>(un.g) * p.idx_sh;
+    const int32_t e_ask = key_entry<kBlocks>(p, list, un, wi * kGroup + lane);
+    Walk::cut(p, un);
+    const int32_t e_first = wi * kGroup + lane < un.n_eff ? e_ask : -1;
     const int32_t last = kBlocks ? last_visible(p, un.t) : 0x7fffffff;
     const char* kc = fp.codes[0] + un.g * fp.c_sh;
     const char* vc = fp.codes[1] + un.g * fp.c_sh;
@@ -695,7 +708,6 @@ __global__ void __launch_bounds__(kThreadsN, 1) qsa_attn_f4_narrow_kernel(const 
       if (i < groups) gather(st + kOffV, st + kOffVs, vc, vb, fp.c_ss, fp.b_ss, id, m, lane);
       cp_async_commit();
     };
-    const int32_t e_first = entry(wi);
     constexpr int kQ = (8 + W - 1) / W;                 // heads this warp prepares
     uint4 qv[kQ];
     if (groups > 0) {
