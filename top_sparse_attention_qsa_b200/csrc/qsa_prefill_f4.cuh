@@ -367,13 +367,7 @@ __global__ void __launch_bounds__(kThreads4, 1) qsa_attn_f4_kernel(const __grid_
     int stage = 0;
     for (int i = wi; i < groups; i += W, stage ^= 1) {
       const uint32_t mask = mask_next;
-      if (i + W < groups) {
-        issue(i + W, stage ^ 1, e_next);
-        e_next = entry(i + 2 * W);
-        cp_async_wait<1>();
-      } else {
-        cp_async_wait<0>();
-      }
+      cp_async_wait<0>();
       __syncwarp();
       const uint32_t st = ring + stage * kStageBytes;
 
@@ -416,6 +410,13 @@ __global__ void __launch_bounds__(kThreads4, 1) qsa_attn_f4_kernel(const __grid_
         }
       }
 
+      // the next group's rows, asked for here: ahead of the scores their 18
+      // copies and addresses held up the K reads (2.44 against 2.12 ms)
+      if (i + W < groups) {
+        issue(i + W, stage ^ 1, e_next);
+        e_next = entry(i + 2 * W);
+      }
+
       // x = s - mx, p = 2^x; s[t] = {head n: keys 2j, 2j+1; head n + 8: the same} of tile t
       float x[4][4];
       float top = -INFINITY;
@@ -426,9 +427,18 @@ __global__ void __launch_bounds__(kThreads4, 1) qsa_attn_f4_kernel(const __grid_
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           x[t][r] = fmaf(s[t][r], qs[r >> 1], -mx[r >> 1]);
-          if (!full) x[t][r] = (mine >> (8 * t + (r & 1))) & 1u ? x[t][r] : -INFINITY;
           top = fmaxf(top, x[t][r]);
         }
+      if (!full) {                                      // some key is masked
+        top = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            x[t][r] = (mine >> (8 * t + (r & 1))) & 1u ? x[t][r] : -INFINITY;
+            top = fmaxf(top, x[t][r]);
+          }
+      }
       if (__any_sync(0xffffffffu, top > kOver)) {
         // raise the running max (always for a unit's first keys): sums and
         // output scale by 2^(m_old - m_new)
@@ -799,9 +809,18 @@ __global__ void __launch_bounds__(kThreadsN, 1) qsa_attn_f4_narrow_kernel(const 
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           x[t][r] = fmaf(s[t][r], qs[r & 1], -mx[r & 1]);
-          if (!full) x[t][r] = (mine >> (16 * t + 8 * (r >> 1))) & 1u ? x[t][r] : -INFINITY;
           top = fmaxf(top, x[t][r]);
         }
+      if (!full) {                                      // some key is masked
+        top = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            x[t][r] = (mine >> (16 * t + 8 * (r >> 1))) & 1u ? x[t][r] : -INFINITY;
+            top = fmaxf(top, x[t][r]);
+          }
+      }
       if (__any_sync(0xffffffffu, top > kOver)) {
         float alpha[2];
 #pragma unroll
