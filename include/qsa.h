@@ -592,11 +592,18 @@ qsa_status_t qsa_sparse_prefill_fp4_fwd(
     void* out, float* lse, int32_t* status, void* stream);
 
 /*
- * Split-K decode over a 4-bit cache: qsa_sparse_decode_fwd's chunking,
- * workspace (qsa_sparse_decode_workspace_bytes) and log-sum-exp merge, with
- * the chunks computed by the kernel of qsa_sparse_prefill_fp4_fwd over token
- * lists.
+ * Split-K decode over a 4-bit cache: qsa_sparse_decode_fwd's chunking and
+ * log-sum-exp merge, with the chunks computed by the kernel of
+ * qsa_sparse_prefill_fp4_fwd over token lists.  Where the 2 to 8 chunks of
+ * every list fit on the device as resident clusters, they run and merge in
+ * one launch and need no workspace; otherwise the partial results go to
+ * `workspace` as in qsa_sparse_decode_fwd.
+ * qsa_sparse_decode_fp4_workspace_bytes says how many bytes that is for this
+ * shape, num_splits and the current device (0: `workspace` may be NULL).
  */
+size_t qsa_sparse_decode_fp4_workspace_bytes(const qsa_shape_t* shape,
+                                             int32_t num_splits);
+
 qsa_status_t qsa_sparse_decode_fp4_fwd(
     const qsa_shape_t* shape, const void* q, const void* k_codes,
     const void* k_bscale, const void* v_codes, const void* v_bscale,

@@ -259,16 +259,23 @@ def test_far_slots(C):
     assert torch.equal(out, want) and torch.equal(lse, wl)
 
 
-@pytest.mark.parametrize("splits", [0, 1, 3, 16])
-def test_split_k_decode(C, splits):
-    T, ctx, heads, K = 6, 700, (24, 2), 650
+@pytest.mark.parametrize("heads", [(24, 2), (16, 2)])
+@pytest.mark.parametrize("T,splits", [(6, 0), (6, 1), (6, 3), (6, 16), (7, 6), (40, 3)])
+def test_split_k_decode(C, heads, T, splits):
+    """One chunk, chunks merged in a cluster (where they fit) and through the workspace."""
+    ctx, K = 700, 650
     q, cache, ks, vs, g = case(C, T, T * ctx, heads, seed=61)
     idx = W.random_lists(T, 2, K, ctx, g, DEV) + (torch.arange(T, dtype=torch.int32, device=DEV) * ctx).view(T, 1, 1)
     nv = torch.full((T, 2), K, dtype=torch.int32, device=DEV)
     nv[1], nv[2], nv[3, 0] = 0, 300, 1
-    out, lse = C.sparse_decode_fp4_fwd(q, cache, idx, ks, vs, n_valid=nv, num_splits=splits)
+    need = C.decode_fp4_workspace_bytes(q, cache, idx, splits)
+    ws = torch.full((need + 256,), 0xff, dtype=torch.uint8, device=DEV)
+    out, lse = C.sparse_decode_fp4_fwd(q, cache, idx, ks, vs, n_valid=nv, num_splits=splits, workspace=ws)
     torch.cuda.synchronize()
-    assert compare(out, lse, reference(q, cache, ks, vs, idx, nv), f"decode splits={splits}") == 24
+    assert compare(out, lse, reference(q, cache, ks, vs, idx, nv), f"decode splits={splits}") == heads[0]
+    again, _ = C.sparse_decode_fp4_fwd(q, cache, idx, ks, vs, n_valid=nv, num_splits=splits)
+    torch.cuda.synchronize()
+    assert torch.equal(again, out)
 
 
 def test_append_then_decode(C):

@@ -13,7 +13,7 @@ _API = ("sparse_prefill_fwd", "sparse_prefill_debug_gather", "sparse_prefill_fwd
         "decode_workspace_bytes", "decode_num_splits",
         "indexer_scores", "topk_select", "indexer_select",
         "kv_append", "kv_append_fp8", "kv_append_fp4", "Fp4Cache", "fp4_cache", "rope_table",
-        "sparse_prefill_fp4_fwd", "sparse_decode_fp4_fwd",
+        "sparse_prefill_fp4_fwd", "sparse_decode_fp4_fwd", "decode_fp4_workspace_bytes",
         "status_string", "abi_version", "QSAError", "STATUS_OOB_SLOT", "STATUS_TIMEOUT", "STATUS_BAD_POSITION")
 
 

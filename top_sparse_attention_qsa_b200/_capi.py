@@ -40,7 +40,7 @@ EXPORTS = ("qsa_sparse_prefill_fwd", "qsa_sparse_prefill_fwd_with", "qsa_sparse_
            "qsa_sparse_decode_num_splits", "qsa_sparse_decode_fwd_noalloc",
            "qsa_sparse_prefill_fp8_fwd", "qsa_sparse_decode_fp8_fwd", "qsa_indexer_scores",
            "qsa_indexer_fold_heads", "qsa_topk_select", "qsa_kv_append", "qsa_kv_append_fp8", "qsa_kv_append_fp4",
-           "qsa_sparse_prefill_fp4_fwd", "qsa_sparse_decode_fp4_fwd", "qsa_status_string", "qsa_abi_version")
+           "qsa_sparse_prefill_fp4_fwd", "qsa_sparse_decode_fp4_fwd", "qsa_sparse_decode_fp4_workspace_bytes", "qsa_status_string", "qsa_abi_version")
 
 
 class Shape(ctypes.Structure):
@@ -160,6 +160,8 @@ _lib.qsa_sparse_prefill_fp4_fwd.argtypes = ([_vp, ctypes.c_int32] + [_vp] * 6 + 
 _lib.qsa_sparse_decode_fp4_fwd.argtypes = ([_vp] * 6 + [ctypes.c_int64] * 2 + [_vp] * 2
                                            + [ctypes.c_float] * 3 + [_vp] * 3
                                            + [ctypes.c_int32, _vp, ctypes.c_size_t, _vp])
+_lib.qsa_sparse_decode_fp4_workspace_bytes.restype = ctypes.c_size_t
+_lib.qsa_sparse_decode_fp4_workspace_bytes.argtypes = [ctypes.POINTER(Shape), ctypes.c_int32]
 _lib.qsa_status_string.restype = ctypes.c_char_p
 _lib.qsa_status_string.argtypes = [ctypes.c_int]
 _lib.qsa_abi_version.restype = ctypes.c_int32
@@ -801,11 +803,19 @@ def sparse_prefill_fp4_fwd(q, cache: Fp4Cache, topk_idx, k_scale: float, v_scale
                                         last_slot, 0, None, out, lse, status, stream, want_lse))
 
 
+def decode_fp4_workspace_bytes(q, cache: Fp4Cache, topk_idx, num_splits: int = 0) -> int:
+    """Scratch bytes sparse_decode_fp4_fwd needs on q's device: 0 for a single
+    chunk, and for chunks that run as one cluster."""
+    shape = make_shape(q, cache.buffer, topk_idx, q)
+    with torch.cuda.device(q.device):
+        return int(_lib.qsa_sparse_decode_fp4_workspace_bytes(ctypes.byref(shape), int(num_splits)))
+
+
 def sparse_decode_fp4_fwd(q, cache: Fp4Cache, topk_idx, k_scale: float, v_scale: float, n_valid=None,
                           scale: float = 0.0, num_splits: int = 0, workspace=None, out=None, lse=None, status=None,
                           stream=None, want_lse: bool = True):
     """Split-K decode over a 4-bit cache.  A workspace of
-    decode_workspace_bytes(q, cache.k_codes, topk_idx, num_splits) bytes is
-    allocated when none is given.  Returns (out, lse)."""
+    decode_fp4_workspace_bytes(...) bytes is allocated when none is given.
+    Returns (out, lse)."""
     return _outputs(_binding.sparse_fp4(1, q, cache.buffer, topk_idx, k_scale, v_scale, n_valid, scale, 1, None,
                                         num_splits, workspace, out, lse, status, stream, want_lse))

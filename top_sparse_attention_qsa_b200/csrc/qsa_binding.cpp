@@ -311,7 +311,7 @@ PyObject* sparse_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
         need(ws.is_cuda() && ws.get_device() == dev && ws.is_contiguous(), "workspace must be a contiguous CUDA tensor");
         bytes = ws.numel() * ws.element_size();
       } else {
-        bytes = qsa_sparse_decode_workspace_bytes(&s, splits);
+        bytes = qsa_sparse_decode_fp4_workspace_bytes(&s, splits);
         if (bytes > 0) ws = at::empty({static_cast<int64_t>(bytes)}, buf.options());
       }
       rc = qsa_sparse_decode_fp4_fwd(&s, q.data_ptr(), c, c + 256, c + 128, c + 272, buf.stride(0), buf.stride(1), list,

@@ -251,5 +251,69 @@ cudaError_t launch_f4(const qsa::f4::F4Params& fp, cudaStream_t stream) {
   }
 }
 
+// The cluster form of a decode (qsa_prefill_f4.cuh): a CTA per chunk, the
+// chunks of a list one cluster.
+template <typename Kernel>
+cudaError_t f4_cluster_config(Kernel kernel, int threads, int smem, std::atomic<int>* done, int64_t units, int chunks,
+                              cudaLaunchConfig_t* cfg, cudaLaunchAttribute* at, cudaStream_t stream) {
+  const cudaError_t e = set_smem_once(kernel, smem, done);
+  if (e != cudaSuccess) return e;
+  at->id = cudaLaunchAttributeClusterDimension;
+  at->val.clusterDim.x = chunks;
+  at->val.clusterDim.y = at->val.clusterDim.z = 1;
+  cfg->gridDim = dim3(static_cast<unsigned>(units));
+  cfg->blockDim = dim3(threads);
+  cfg->dynamicSmemBytes = smem;
+  cfg->stream = stream;
+  cfg->attrs = at;
+  cfg->numAttrs = 1;
+  return cudaSuccess;
+}
+
+constexpr int kMaxCluster = 8;
+
+// Calls f(kernel, threads, shared memory, once-flags) with the kernel for groups of G heads.
+template <typename F>
+auto with_f4_cluster_kernel(int G, F f) {
+  using namespace qsa::f4;
+  static std::atomic<int> done[2][kMaxDevices];
+  return G <= 8 ? f(qsa_attn_f4_narrow_kernel<false, kWarpsN, true>, kThreadsN, N_SMEM, done[1])
+                : f(qsa_attn_f4_kernel<false, kWarps4, true>, kThreads4, H_SMEM, done[0]);
+}
+
+// Whether `lists` lists of `chunks` chunks run as clusters that are all
+// resident at once (a second wave would cost more than the merge launch).
+inline bool f4_cluster_fits(int G, int64_t lists, int chunks) {
+  static std::atomic<int> most[2][kMaxCluster + 1][kMaxDevices];   // clusters resident at once, + 1
+  int dev = 0;
+  if (chunks < 2 || chunks > kMaxCluster || lists * chunks > sm_count()) return false;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+  std::atomic<int>& slot = most[G <= 8 ? 1 : 0][chunks][dev];
+  int n = slot.load(std::memory_order_relaxed);
+  if (n == 0) {
+    n = with_f4_cluster_kernel(G, [&](auto kernel, int threads, int smem, std::atomic<int>* done) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute at = {};
+      int k = 0;
+      if (f4_cluster_config(kernel, threads, smem, done, chunks, chunks, &cfg, &at, nullptr) != cudaSuccess ||
+          cudaOccupancyMaxActiveClusters(&k, kernel, &cfg) != cudaSuccess)
+        return 1;
+      return k + 1;
+    });
+    slot.store(n, std::memory_order_relaxed);
+  }
+  return lists <= n - 1;
+}
+
+inline cudaError_t launch_f4_cluster(const qsa::f4::F4Params& fp, cudaStream_t stream) {
+  return with_f4_cluster_kernel(fp.t.G, [&](auto kernel, int threads, int smem, std::atomic<int>* done) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at = {};
+    const cudaError_t e = f4_cluster_config(kernel, threads, smem, done, fp.t.T * fp.t.Hkv * fp.t.splits, fp.t.splits,
+                                            &cfg, &at, stream);
+    return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kernel, fp);
+  });
+}
+
 }  // namespace launch
 }  // namespace qsa

@@ -157,6 +157,79 @@ __device__ __forceinline__ __half2 scales2(uint32_t two_bytes) {
   return *reinterpret_cast<const __half2*>(&h);
 }
 
+// ------------------------------------------------------------------ clusters
+
+// A decode list cut into up to 8 chunks can run as one cluster, a CTA per
+// chunk: each leaves its chunk's max, sum and unnormalised output in its
+// shared memory, and the cluster merges them from there, without a workspace
+// and a second launch.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
+__device__ __forceinline__ float cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(addr));
+  return v;
+}
+
+__device__ __forceinline__ float4 cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+
+// A chunk's result in shared memory: O [16][256], then max - 7 [16] and sum [16].
+constexpr int kPartO = 0, kPartM = 16 * 256 * 4, kPartL = kPartM + 64, kPartBytes = kPartL + 64;
+
+// Warp `w` of the cluster's `warps` merges heads w, w + warps, ... of the
+// chunks' results at `part` of every CTA; put(h, max, sum, first 4 dims of the
+// lane's 8, other 4) gets each, unnormalised.
+template <typename Put>
+__device__ __forceinline__ void cluster_merge(uint32_t part, int chunks, int G, int w, int warps, int lane, Put put) {
+  for (int h = w; h < G; h += warps) {
+    // every chunk's numbers at once: one trip through the cluster, not one a chunk
+    float m[8], ls[8];
+    float4 x[8], y[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      m[c] = -INFINITY;
+      if (c < chunks) {
+        const uint32_t at = cluster_addr(part, c);
+        m[c] = cluster_f32(at + kPartM + 4 * h);
+        ls[c] = cluster_f32(at + kPartL + 4 * h);
+        x[c] = cluster_f32x4(at + kPartO + h * 1024 + lane * 32);
+        y[c] = cluster_f32x4(at + kPartO + h * 1024 + lane * 32 + 16);
+      }
+    }
+    float M = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) M = fmaxf(M, m[c]);
+    float4 a = {}, b = {};
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      if (c >= chunks) continue;
+      const float f = m[c] == M ? 1.f : ex2(m[c] - M);   // a chunk without a key: 0
+      l += ls[c] * f;
+      a = make_float4(fmaf(x[c].x, f, a.x), fmaf(x[c].y, f, a.y), fmaf(x[c].z, f, a.z), fmaf(x[c].w, f, a.w));
+      b = make_float4(fmaf(y[c].x, f, b.x), fmaf(y[c].y, f, b.y), fmaf(y[c].z, f, b.z), fmaf(y[c].w, f, b.w));
+    }
+    put(h, M, l, a, b);
+  }
+}
+
 // ------------------------------------------------------------------ units
 
 // The units of slot blockIdx.x + gridDim.x * (warp / W), then every gridDim.x *
@@ -295,7 +368,7 @@ __device__ __forceinline__ void q_head(const TcParams& p, const uint4& v, uint32
 
 // ------------------------------------------------------------------ kernel
 
-template <bool kBlocks, int W>
+template <bool kBlocks, int W, bool kCluster = false>
 __global__ void __launch_bounds__(kThreads4, 1) qsa_attn_f4_kernel(const __grid_constant__ F4Params fp) {
   extern __shared__ __align__(1024) uint8_t sm[];
   const TcParams& p = fp.t;
@@ -317,6 +390,15 @@ __global__ void __launch_bounds__(kThreads4, 1) qsa_attn_f4_kernel(const __grid_
     Unit un = wk.unit(p);
     const int32_t* list = p.idx + un.t * p.idx_st + static_cast<int64_t>(un.g) * p.idx_sh;
     const int32_t e_ask = key_entry<kBlocks>(p, list, un, wi * kGroup + lane);
+    // every load of Q at once; where a unit is short (several warps to it, or
+    // a chunk of a cluster) with the list's first load, else behind it
+    constexpr bool kEarlyQ = kCluster || (W > 1 && W < kWarps4);
+    uint4 qv[16 / W];
+    auto ask_q = [&] {
+#pragma unroll
+      for (int h = 0; h < 16 / W; ++h) qv[h] = q_load(p, un, wi + h * W, lane);
+    };
+    if (kEarlyQ) ask_q();
     Walk::cut(p, un);
     const int32_t e_first = wi * kGroup + lane < un.n_eff ? e_ask : -1;
     const int32_t last = kBlocks ? last_visible(p, un.t) : 0x7fffffff;
@@ -340,11 +422,7 @@ __global__ void __launch_bounds__(kThreads4, 1) qsa_attn_f4_kernel(const __grid_
       cp_async_commit();
     };
     int32_t e_next = e_first;
-    uint4 qv[16 / W];                                   // every load of Q at once, behind the list's
-    if (groups > 0) {
-#pragma unroll
-      for (int h = 0; h < 16 / W; ++h) qv[h] = q_load(p, un, wi + h * W, lane);
-    }
+    if (!kEarlyQ && groups > 0) ask_q();
     if (wi < groups) issue(wi, 0, e_next);
     e_next = entry(wi + W);
     // Q, while the first rows are on their way
@@ -585,6 +663,8 @@ __global__ void __launch_bounds__(kThreads4, 1) qsa_attn_f4_kernel(const __grid_
       }
     }
     sync_unit();
+    uint8_t* part = sm + H_Q;                           // (Q is read)
+    static_assert(kPartBytes <= kWarps4 * kQTile, "a chunk's result fits where Q was");
     float* slab0 = reinterpret_cast<float*>(sm + H_RING + grp * W * kStages * kStageBytes);
     constexpr int kSlab = kStages * kStageBytes / 4;
 #pragma unroll
@@ -612,8 +692,8 @@ __global__ void __launch_bounds__(kThreads4, 1) qsa_attn_f4_kernel(const __grid_
         const float m = ml[w * 32 + h];
         lt += ml[w * 32 + 16 + h] * (m == M ? 1.f : ex2(m - M));
       }
-      if (lane == 0) put_lse(h, lt, M);
-      const float inv = lt == 0.f ? 0.f : p.o_scale / lt;
+      if (lane == 0 && !kCluster) put_lse(h, lt, M);
+      const float inv = kCluster ? 1.f : lt == 0.f ? 0.f : p.o_scale / lt;
       float4 acc[2] = {};
 #pragma unroll
       for (int c = 0; c < 2; ++c) {                     // chunks 2 lane, 2 lane + 1: dims 8 lane ..
@@ -630,7 +710,15 @@ __global__ void __launch_bounds__(kThreads4, 1) qsa_attn_f4_kernel(const __grid_
         acc[c].z *= inv;
         acc[c].w *= inv;
       }
-      if (p.part_o != nullptr) {
+      if (kCluster) {
+        float4* dst = reinterpret_cast<float4*>(part + kPartO + h * 1024) + 2 * lane;
+        dst[0] = acc[0];
+        dst[1] = acc[1];
+        if (lane == 0) {
+          *reinterpret_cast<float*>(part + kPartM + 4 * h) = M;
+          *reinterpret_cast<float*>(part + kPartL + 4 * h) = lt;
+        }
+      } else if (p.part_o != nullptr) {
         float4* dst = reinterpret_cast<float4*>(p.part_o + ((row0 + h) * p.splits + un.s) * 256) + 2 * lane;
         dst[0] = acc[0];
         dst[1] = acc[1];
@@ -639,6 +727,20 @@ __global__ void __launch_bounds__(kThreads4, 1) qsa_attn_f4_kernel(const __grid_
             make_uint4(pack_bf16x2(acc[0].x, acc[0].y), pack_bf16x2(acc[0].z, acc[0].w),
                        pack_bf16x2(acc[1].x, acc[1].y), pack_bf16x2(acc[1].z, acc[1].w));
       }
+    }
+    if (kCluster) {                                     // (one unit to a CTA)
+      cluster_sync();
+      cluster_merge(smem_u32(part), p.splits, p.G, static_cast<int>(cluster_rank()) * W + wi, p.splits * W, lane,
+                    [&](int h, float M, float lt, const float4& a, const float4& b) {
+                      if (lane == 0) put_lse(h, lt, M);
+                      const float inv = lt == 0.f ? 0.f : p.o_scale / lt;
+                      *reinterpret_cast<uint4*>(p.out + un.t * p.o_st +
+                                                (static_cast<int64_t>(un.g) * p.G + h) * p.o_sh + 8 * lane) =
+                          make_uint4(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv),
+                                     pack_bf16x2(b.x * inv, b.y * inv), pack_bf16x2(b.z * inv, b.w * inv));
+                    });
+      cluster_sync();                                   // the other CTAs have read this one's part
+      return;
     }
     sync_unit();                                        // slabs and Q are read before the next unit's
   }
@@ -674,7 +776,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   return r;
 }
 
-template <bool kBlocks, int W>
+template <bool kBlocks, int W, bool kCluster = false>
 __global__ void __launch_bounds__(kThreadsN, 1) qsa_attn_f4_narrow_kernel(const __grid_constant__ F4Params fp) {
   extern __shared__ __align__(1024) uint8_t sm[];
   const TcParams& p = fp.t;
@@ -696,6 +798,10 @@ __global__ void __launch_bounds__(kThreadsN, 1) qsa_attn_f4_narrow_kernel(const 
     Unit un = wk.unit(p);
     const int32_t* list = p.idx + un.t * p.idx_st + static_cast<int64_t>(un.g) * p.idx_sh;
     const int32_t e_ask = key_entry<kBlocks>(p, list, un, wi * kGroup + lane);
+    constexpr int kQ = (8 + W - 1) / W;                 // heads this warp prepares
+    uint4 qv[kQ];
+#pragma unroll
+    for (int h = 0; h < kQ; ++h) qv[h] = q_load(p, un, wi + h * W, lane);
     Walk::cut(p, un);
     const int32_t e_first = wi * kGroup + lane < un.n_eff ? e_ask : -1;
     const int32_t last = kBlocks ? last_visible(p, un.t) : 0x7fffffff;
@@ -723,12 +829,6 @@ __global__ void __launch_bounds__(kThreadsN, 1) qsa_attn_f4_narrow_kernel(const 
       if (i < groups) gather(st + kOffV, st + kOffVs, vc, vb, fp.c_ss, fp.b_ss, id, m, lane);
       cp_async_commit();
     };
-    constexpr int kQ = (8 + W - 1) / W;                 // heads this warp prepares
-    uint4 qv[kQ];
-    if (groups > 0) {
-#pragma unroll
-      for (int h = 0; h < kQ; ++h) qv[h] = q_load(p, un, wi + h * W, lane);
-    }
     int32_t id = resolve(wi, e_first);
     uint32_t mask = __ballot_sync(0xffffffffu, id >= 0);
     issue_k(wi, id, mask);
@@ -952,6 +1052,8 @@ __global__ void __launch_bounds__(kThreadsN, 1) qsa_attn_f4_narrow_kernel(const 
       }
     }
     sync_unit();
+    uint8_t* part = sm + N_Q;                           // (Q is read)
+    static_assert(kPartBytes <= kWarpsN * kQTileN, "a chunk's result fits where Q was");
     float* slab0 = reinterpret_cast<float*>(sm + N_RING + grp * W * kStageBytes);
     constexpr int kSlab = kStageBytes / 4;
 #pragma unroll
@@ -975,8 +1077,8 @@ __global__ void __launch_bounds__(kThreadsN, 1) qsa_attn_f4_narrow_kernel(const 
         const float m = ml[w * 16 + h];
         lt += ml[w * 16 + 8 + h] * (m == M ? 1.f : ex2(m - M));
       }
-      if (lane == 0) put_lse(h, lt, M);
-      const float inv = lt == 0.f ? 0.f : p.o_scale / lt;
+      if (lane == 0 && !kCluster) put_lse(h, lt, M);
+      const float inv = kCluster ? 1.f : lt == 0.f ? 0.f : p.o_scale / lt;
       float4 acc[2] = {};
 #pragma unroll
       for (int c = 0; c < 2; ++c) {                     // chunks 2 lane, 2 lane + 1: dims 8 lane ..
@@ -993,7 +1095,15 @@ __global__ void __launch_bounds__(kThreadsN, 1) qsa_attn_f4_narrow_kernel(const 
         acc[c].z *= inv;
         acc[c].w *= inv;
       }
-      if (p.part_o != nullptr) {
+      if (kCluster) {
+        float4* dst = reinterpret_cast<float4*>(part + kPartO + h * 1024) + 2 * lane;
+        dst[0] = acc[0];
+        dst[1] = acc[1];
+        if (lane == 0) {
+          *reinterpret_cast<float*>(part + kPartM + 4 * h) = M;
+          *reinterpret_cast<float*>(part + kPartL + 4 * h) = lt;
+        }
+      } else if (p.part_o != nullptr) {
         float4* dst = reinterpret_cast<float4*>(p.part_o + ((row0 + h) * p.splits + un.s) * 256) + 2 * lane;
         dst[0] = acc[0];
         dst[1] = acc[1];
@@ -1002,6 +1112,20 @@ __global__ void __launch_bounds__(kThreadsN, 1) qsa_attn_f4_narrow_kernel(const 
             make_uint4(pack_bf16x2(acc[0].x, acc[0].y), pack_bf16x2(acc[0].z, acc[0].w),
                        pack_bf16x2(acc[1].x, acc[1].y), pack_bf16x2(acc[1].z, acc[1].w));
       }
+    }
+    if (kCluster) {                                     // (one unit to a CTA)
+      cluster_sync();
+      cluster_merge(smem_u32(part), p.splits, p.G, static_cast<int>(cluster_rank()) * W + wi, p.splits * W, lane,
+                    [&](int h, float M, float lt, const float4& a, const float4& b) {
+                      if (lane == 0) put_lse(h, lt, M);
+                      const float inv = lt == 0.f ? 0.f : p.o_scale / lt;
+                      *reinterpret_cast<uint4*>(p.out + un.t * p.o_st +
+                                                (static_cast<int64_t>(un.g) * p.G + h) * p.o_sh + 8 * lane) =
+                          make_uint4(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv),
+                                     pack_bf16x2(b.x * inv, b.y * inv), pack_bf16x2(b.z * inv, b.w * inv));
+                    });
+      cluster_sync();                                   // the other CTAs have read this one's part
+      return;
     }
     sync_unit();                                        // slabs and Q are read before the next unit's
   }
