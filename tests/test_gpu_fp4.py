@@ -71,7 +71,7 @@ def compare(out, lse, ref, label=""):
     d = np.abs(o - ro)[~empty]
     worst = float((d / bo[~empty]).max())
     assert worst <= 1, f"{label}: out off by {d.max():.3e}, {worst:.2f} of the bound"
-    d = np.abs(l - rl)[~empty]
+    d = np.abs(l[~empty] - rl[~empty])
     worst = float((d / bl[~empty]).max())
     assert worst <= 1, f"{label}: lse off by {d.max():.3e}, {worst:.2f} of the bound"
     return int(empty.sum())
@@ -152,6 +152,56 @@ def test_runs_of_empty_units(C):
     t = np.arange(0, T, 7)
     ref = reference(q, cache, ks, vs, idx, nv, tokens=list(t))
     compare(out[torch.from_numpy(t)], lse[torch.from_numpy(t)], ref, "empty units")
+
+
+@pytest.mark.parametrize("heads", [(12, 1), (6, 1)])
+@pytest.mark.parametrize("T", [100, 250, 500, 1400])
+def test_warps_per_unit(C, heads, T):
+    """Numbers of units for which a unit is worked by 8 (12), 4, 2 warps and by one."""
+    S, K = 900, 600
+    q, cache, ks, vs, g = case(C, T, S, heads, seed=T + heads[0])
+    idx = W.random_lists(T, 1, K, S, g, DEV)
+    nv = torch.randint(0, K + 1, (T, 1), generator=g, device=DEV, dtype=torch.int32)
+    nv[::5] = K
+    nv[3] = 0
+    out, lse = C.sparse_prefill_fp4_fwd(q, cache, idx, ks, vs, n_valid=nv)
+    torch.cuda.synchronize()
+    t = sorted({0, 1, 2, 3, T - 2, T - 1, *range(0, T, 29)})
+    ti = torch.tensor(t)
+    assert compare(out[ti], lse[ti], reference(q, cache, ks, vs, idx, nv, tokens=t), f"T={T}") >= heads[0]
+
+
+def test_two_streams_at_once(C):
+    """Appends and decodes of two batches on two streams, as when each runs alone."""
+    runs = []
+    for seed in (81, 82):
+        q, cache, ks, vs, g = case(C, 9, 4000, (24, 2), seed)
+        k, v = (torch.randn((9, 2, 256), generator=g, device=DEV).to(torch.bfloat16) for _ in "kv")
+        pos = torch.randint(0, 4000, (9,), generator=g, device=DEV, dtype=torch.int32)
+        slots = torch.randperm(4000, generator=g, device=DEV)[:9].to(torch.int32)
+        idx = W.random_lists(9, 2, 1500, 4000, g, DEV)
+        idx[:, :, 0] = slots.view(9, 1)
+        runs.append((q, cache, ks, vs, k, v, pos, slots, idx))
+    table = C.rope_table(4000, 64, device=DEV)
+
+    def step(r, cache):
+        q, _, ks, vs, k, v, pos, slots, idx = r
+        qr, _, _ = C.kv_append_fp4(k, v, pos, slots, table, cache, ks, vs, q=q)
+        return C.sparse_decode_fp4_fwd(qr, cache, idx, ks, vs)
+
+    alone = [step(r, C.Fp4Cache(r[1].buffer.clone())) for r in runs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in runs]
+    for _ in range(5):
+        caches = [C.Fp4Cache(r[1].buffer.clone()) for r in runs]
+        torch.cuda.synchronize()
+        outs = []
+        for r, c, s in zip(runs, caches, streams):
+            with torch.cuda.stream(s):
+                outs.append(step(r, c))
+        torch.cuda.synchronize()
+        for (o, l), (wo, wl) in zip(outs, alone):
+            assert torch.equal(o, wo) and torch.equal(l, wl)
 
 
 @pytest.mark.parametrize("bs", [1, 2, 4, 16])
