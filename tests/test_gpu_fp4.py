@@ -328,6 +328,44 @@ def test_split_k_decode(C, heads, T, splits):
     assert torch.equal(again, out)
 
 
+def test_workspace_belongs_to_the_launching_stream(C):
+    """An allocated workspace is let go on return, with its kernels still to run:
+    only work of the same stream may be given its memory."""
+    heads, T, ctx, K = (24, 2), 40, 700, 650           # 240 chunks: more than run at once
+    q, cache, ks, vs, g = case(C, T, T * ctx, heads, seed=62)
+    idx = W.random_lists(T, 2, K, ctx, g, DEV) + (torch.arange(T, dtype=torch.int32, device=DEV) * ctx).view(T, 1, 1)
+    assert C.decode_fp4_workspace_bytes(q, cache, idx, 3) > 0
+    want, wl = C.sparse_decode_fp4_fwd(q, cache, idx, ks, vs, num_splits=3)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    held = lambda: sum(x["total_size"] for x in torch.cuda.memory_snapshot() if x["stream"] == side.cuda_stream)
+    before = held()
+    side.wait_stream(torch.cuda.current_stream())
+    out, lse = C.sparse_decode_fp4_fwd(q, cache, idx, ks, vs, num_splits=3, stream=side.cuda_stream)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    assert held() > before
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+def test_signs_repeats_and_ranges(C):
+    """Negative tensor scales, a row named more than once, and integers past 32 bits."""
+    T, S, heads = 5, 400, (24, 2)
+    q, cache, ks, vs, g = case(C, T, S, heads, seed=63)
+    idx = W.random_lists(T, 2, 300, S, g, DEV)
+    idx[:, :, 200:] = idx[:, :, :100]
+    idx[1] = 17
+    for a, b in ((ks, vs), (-ks, vs), (ks, -vs)):
+        for f in (C.sparse_prefill_fp4_fwd, C.sparse_decode_fp4_fwd):
+            out, lse = f(q, cache, idx, a, b)
+            torch.cuda.synchronize()
+            compare(out, lse, reference(q, cache, a, b, idx), f"{f.__name__} {a} {b}")
+    with pytest.raises(ValueError):
+        C.sparse_prefill_fp4_fwd(q, cache, idx, ks, vs, block_size=(1 << 32) + 1)
+    with pytest.raises(ValueError):
+        C.sparse_decode_fp4_fwd(q, cache, idx, ks, vs, num_splits=1 << 32)
+
+
 def test_append_then_decode(C):
     """The run of a serving step: rows appended, then attention whose lists name
     them, captured once and replayed with other contents."""

@@ -815,7 +815,9 @@ def sparse_decode_fp4_fwd(q, cache: Fp4Cache, topk_idx, k_scale: float, v_scale:
                           scale: float = 0.0, num_splits: int = 0, workspace=None, out=None, lse=None, status=None,
                           stream=None, want_lse: bool = True):
     """Split-K decode over a 4-bit cache.  A workspace of
-    decode_fp4_workspace_bytes(...) bytes is allocated when none is given.
-    Returns (out, lse)."""
+    decode_fp4_workspace_bytes(...) bytes is allocated (for the launching
+    stream) when none is given; one that is given serves one call at a time, so
+    calls or captured graphs that may run at once need one each.  Returns
+    (out, lse)."""
     return _outputs(_binding.sparse_fp4(1, q, cache.buffer, topk_idx, k_scale, v_scale, n_valid, scale, 1, None,
                                         num_splits, workspace, out, lse, status, stream, want_lse))

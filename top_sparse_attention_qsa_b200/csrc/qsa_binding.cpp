@@ -75,6 +75,18 @@ int64_t integer(PyObject* o) {
   return x;
 }
 
+int32_t integer32(PyObject* o, const char* name) {
+  const int64_t x = integer(o);
+  if (x != static_cast<int32_t>(x)) throw ValueFault(std::string(name) + " is out of range");
+  return static_cast<int32_t>(x);
+}
+
+// A size as the C ABI's 32 bits.
+int32_t size32(int64_t n) {
+  need(n <= 0x7fffffff, "a dimension is out of range");
+  return static_cast<int32_t>(n);
+}
+
 void* stream_of(PyObject* o, int dev) {
   if (given(o)) {
     void* s = PyLong_AsVoidPtr(o);
@@ -145,8 +157,8 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
          format == 2 ? "cache must be [S, Hkv, 288]" : "k_cache must be [S, Hkv, 256]");
     qsa_append_shape_t s = {};
     s.num_tokens = k.size(0);
-    s.num_kv_heads = static_cast<int32_t>(k.size(1));
-    s.head_dim = static_cast<int32_t>(k.size(2));
+    s.num_kv_heads = size32(k.size(1));
+    s.head_dim = size32(k.size(2));
     s.num_slots = kc.size(0);
     need(k.stride(2) == 1 && v.stride(2) == 1 && kc.stride(2) == 1, kInner);
     if (format != 2) {
@@ -177,7 +189,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       } else {
         q_out = at::empty(q.sizes(), q.options());
       }
-      s.num_q_heads = static_cast<int32_t>(q.size(1));
+      s.num_q_heads = size32(q.size(1));
       s.q_stride_tok = q.stride(0);
       s.q_stride_head = q.stride(1);
       s.qo_stride_tok = q_out->stride(0);
@@ -247,13 +259,12 @@ PyObject* sparse_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     need(q.dim() == 3 && idx.dim() == 3 && buf.dim() == 3, "q, the cache and topk_idx must be 3-d");
     qsa_shape_t s = {};
     s.num_tokens = q.size(0);
-    s.num_q_heads = static_cast<int32_t>(q.size(1));
-    s.head_dim = static_cast<int32_t>(q.size(2));
+    s.num_q_heads = size32(q.size(1));
+    s.head_dim = size32(q.size(2));
     s.num_slots = buf.size(0);
-    s.num_kv_heads = static_cast<int32_t>(buf.size(1));
+    s.num_kv_heads = size32(buf.size(1));
     need(idx.size(0) == s.num_tokens && idx.size(1) == s.num_kv_heads, "topk_idx must be [T, Hkv, K]");
-    need(idx.size(2) <= 0x7fffffff, "topk_idx has too many entries");
-    s.topk = static_cast<int32_t>(idx.size(2));
+    s.topk = size32(idx.size(2));
     const int32_t* n_valid = nullptr;
     if (given(a[6])) {
       const Tensor& nv = tensor(a[6], "n_valid", at::kInt, dev);
@@ -302,7 +313,7 @@ PyObject* sparse_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
                 scale = static_cast<float>(number(a[7]));
     qsa_status_t rc;
     if (decode) {
-      const int32_t splits = static_cast<int32_t>(integer(a[10]));
+      const int32_t splits = integer32(a[10], "num_splits");
       Tensor ws;
       size_t bytes = 0;
       if (given(a[11])) {
@@ -312,13 +323,19 @@ PyObject* sparse_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
         bytes = ws.numel() * ws.element_size();
       } else {
         bytes = qsa_sparse_decode_fp4_workspace_bytes(&s, splits);
-        if (bytes > 0) ws = at::empty({static_cast<int64_t>(bytes)}, buf.options());
+        if (bytes > 0) {
+          // owned by the launching stream: it is let go on return, before the
+          // kernels have run
+          const c10::cuda::CUDAStreamGuard own(
+              c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), static_cast<c10::DeviceIndex>(dev)));
+          ws = at::empty({static_cast<int64_t>(bytes)}, buf.options());
+        }
       }
       rc = qsa_sparse_decode_fp4_fwd(&s, q.data_ptr(), c, c + 256, c + 128, c + 272, buf.stride(0), buf.stride(1), list,
                                      n_valid, scale, ks, vs, out.data_ptr(), lp, status, splits,
                                      ws.defined() ? ws.data_ptr() : nullptr, bytes, stream);
     } else {
-      rc = qsa_sparse_prefill_fp4_fwd(&s, static_cast<int32_t>(integer(a[8])), last, q.data_ptr(), c, c + 256, c + 128,
+      rc = qsa_sparse_prefill_fp4_fwd(&s, integer32(a[8], "block_size"), last, q.data_ptr(), c, c + 256, c + 128,
                                       c + 272, buf.stride(0), buf.stride(1), list, n_valid, scale, ks, vs,
                                       out.data_ptr(), lp, status, stream);
     }
