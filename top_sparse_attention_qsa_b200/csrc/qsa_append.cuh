@@ -19,20 +19,21 @@
 // wrong neighbour next to a border.  The other formats rotate in FP32 and
 // round once to the cache's type.
 //
-// One warp takes kRows rows (heads of Q, K or V) of one token, 8 dims per lane,
-// so that every global access is 16 bytes per lane and a row is one request;
-// the rows of a token go round its warps, so that the few K and V rows, which
-// cost more than Q's, do not meet in one.
-// It asks for all its rows before the first use and reads the token's cosines
-// and sines once; a lane's rotation partners come from the lane that holds
-// them.  A block scale's 16 dims belong to two adjacent lanes.
+// A warp takes 8 query rows of one token, or 2 K and V rows; every access is 16
+// bytes per lane, and a warp asks for all its rows before the first use.  Query
+// rows are mostly dims that do not turn (192 of 256 at R = 64): those are copied
+// a row at a time, and a lane turns 8 whole pairs of one row, so that the 8
+// rows' rotary dims fill one pass over the lanes.  K and V rows lie 8 dims per
+// lane, as the cache rows do; a lane's rotation partners come from the lane
+// that holds them, a block scale's 16 dims belong to two adjacent lanes.
 //
-// Bound by HBM: 236 MB (T = 8192, heads (24,2), BF16 cache) move in 49 us, 4.8
-// TB/s, 0.73 of the measured copy rate.  One row per warp took 90 us (a row
-// waited for its position, then its angles, then its partners, 512 bytes in
-// flight); four rows with 32 warps to the SM 57 us at 24, 49 at 32 (64
-// registers), 75 at 40 (spills).  The 4-bit append takes 61 us: its codes by
-// FP64 comparisons alone took 93.
+// Bound by HBM: 236 MB (T = 8192, heads (24,2), R = 64, BF16 cache) move in 38
+// us, 6.2 TB/s, 0.95 of the measured copy rate; with a 4-bit cache 242 MB in 44
+// us.  Four rows of any kind per warp, 8 dims per lane, took 49 and 61 us (565
+// warp instructions per four rows, three quarters of the lanes rotating dims
+// that do not turn), one row per warp 90 and 92.  Query rows per warp: 4 take
+// 42 us, 6 38, 12 (spills) 50; K and V rows: 1 take 41 us, 4 as long as 2, but
+// the 4-bit cache's 50 against 44.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -44,7 +45,7 @@
 namespace qsa {
 namespace ap {
 
-constexpr int kWarps = 4, kRows = 4;
+constexpr int kWarps = 4, kRowsQ = 8, kRowsKv = 2;
 constexpr uint32_t kStatusOobSlot = 1u, kStatusBadPosition = 4u;
 
 enum Format { kBf16 = 0, kE4m3 = 1, kE2m1 = 2 };
@@ -234,55 +235,122 @@ __device__ __forceinline__ uint4 values4(uint32_t codes, uint32_t scale_byte, fl
   return pack8(v);
 }
 
+// Query rows h0 .. h0 + n - 1 (n <= kRowsQ) of token t.  The dims past R are copied a
+// row at a time (not at all in place); of the rotary dims a lane takes 8 pairs
+// of one row, with both members, so that nothing is exchanged and lanes whose
+// dims do not turn do not go along with those whose do.
+__device__ __forceinline__ void append_q(const AppendParams& p, int64_t t, int h0, int n, int32_t pos, bool bad,
+                                         int lane) {
+  const int half = p.R >> 1;
+  // plain loads: q_out may be q itself; a lane stores only what it has read
+  const __nv_bfloat16* src = p.q + t * p.q_st + h0 * p.q_sh;
+  __nv_bfloat16* dst = p.q_out + t * p.qo_st + h0 * p.qo_sh;
+  const bool pass = 8 * lane >= p.R && p.q_out != p.q;
+  uint4 own[kRowsQ];
+  if (pass) {
+#pragma unroll
+    for (int i = 0; i < kRowsQ; ++i)
+      if (i < n) own[i] = *reinterpret_cast<const uint4*>(src + i * p.q_sh + 8 * lane);
+  }
+  const uint32_t per_row = p.R >> 4, units = n * per_row;
+  struct Unit {
+    uint4 a, b;
+    int row, at;
+  };
+  auto ask = [&](uint32_t u) {
+    Unit r;
+    r.row = u / per_row;
+    r.at = 8 * (u - r.row * per_row);
+    const __nv_bfloat16* x = src + r.row * p.q_sh + r.at;
+    r.a = *reinterpret_cast<const uint4*>(x);
+    r.b = *reinterpret_cast<const uint4*>(x + half);
+    return r;
+  };
+  uint32_t u = lane;
+  Unit next;
+  if (u < units) next = ask(u);
+  if (bad) return;
+  if (pass) {
+#pragma unroll
+    for (int i = 0; i < kRowsQ; ++i)
+      if (i < n) *reinterpret_cast<uint4*>(dst + i * p.qo_sh + 8 * lane) = own[i];
+  }
+  const float* cs = p.table + pos * p.table_st;
+  for (; u < units; u += 32) {
+    const Unit un = next;
+    const float* c = cs + (p.interleaved ? un.at >> 1 : un.at);
+    const int far = p.interleaved ? half >> 1 : 4;      // the second four angles
+    const float4 c0 = __ldg(reinterpret_cast<const float4*>(c)), c1 = __ldg(reinterpret_cast<const float4*>(c + far));
+    const float4 s0 = __ldg(reinterpret_cast<const float4*>(c + half)),
+                 s1 = __ldg(reinterpret_cast<const float4*>(c + half + far));
+    if (u + 32 < units) next = ask(u + 32);
+    const float cc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+    const float ss[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+    float x[8], z[8], y[8], w[8];
+    unpack8(un.a, x);
+    unpack8(un.b, z);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (p.interleaved) {
+        y[2 * i] = rot(x[2 * i], cc[i], x[2 * i + 1], -ss[i]);
+        y[2 * i + 1] = rot(x[2 * i + 1], cc[i], x[2 * i], ss[i]);
+        w[2 * i] = rot(z[2 * i], cc[4 + i], z[2 * i + 1], -ss[4 + i]);
+        w[2 * i + 1] = rot(z[2 * i + 1], cc[4 + i], z[2 * i], ss[4 + i]);
+      } else {
+#pragma unroll
+        for (int k = 2 * i; k < 2 * i + 2; ++k) {
+          y[k] = rot(x[k], cc[k], z[k], -ss[k]);
+          w[k] = rot(z[k], cc[k], x[k], ss[k]);
+        }
+      }
+    }
+    __nv_bfloat16* o = dst + un.row * p.qo_sh + un.at;
+    *reinterpret_cast<uint4*>(o) = pack8(y);
+    *reinterpret_cast<uint4*>(o + half) = pack8(w);
+  }
+}
+
 template <int kFormat>
 __global__ void __launch_bounds__(32 * kWarps, 8) qsa_append_kernel(const __grid_constant__ AppendParams p) {
-  const int rows = p.Hq + 2 * p.Hkv;
-  const uint32_t per_tok = (rows + kRows - 1) / kRows;
+  const uint32_t q_warps = (p.Hq + kRowsQ - 1) / kRowsQ;
+  const int rows = 2 * p.Hkv, kv_warps = (rows + kRowsKv - 1) / kRowsKv;
+  const uint32_t per_tok = q_warps + kv_warps;
   const uint32_t w = blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  const uint32_t tok = w / per_tok;
+  const uint32_t tok = w / per_tok, place = w - tok * per_tok;
   const int64_t t = tok;
-  const int r0 = static_cast<int>(w - tok * per_tok);    // rows r0, r0 + per_tok, ...
   if (t >= p.T) return;
-  // what depends on the token, and the warp's rows
   const int32_t pos = p.R > 0 ? __ldg(p.positions + t) : 0;
+  const bool bad = p.R > 0 && (pos < 0 || pos >= p.P);
+  if (place < q_warps) {
+    const int share = (p.Hq + q_warps - 1) / q_warps;   // the heads evenly: 12 as 6 and 6
+    const int h0 = place * share;
+    return append_q(p, t, h0, min(share, p.Hq - h0), pos, bad, lane);
+  }
+  const int r0 = static_cast<int>(place - q_warps);     // K and V rows r0, r0 + kv_warps, ...
   const int32_t slot = __ldg(p.slots + t);
-  uint4 own[kRows];
+  uint4 own[kRowsKv];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int r = r0 + i * static_cast<int>(per_tok);
-    // plain loads: q_out may be q itself, and no lane stores before all have read
-    const __nv_bfloat16* src = r < p.Hq ? p.q + t * p.q_st + r * p.q_sh
-                               : r < p.Hq + p.Hkv ? p.k + t * p.k_st + (r - p.Hq) * p.k_sh
-                                                  : p.v + t * p.v_st + (r - p.Hq - p.Hkv) * p.v_sh;
-    if (r < rows) own[i] = *reinterpret_cast<const uint4*>(src + 8 * lane);
+  for (int i = 0; i < kRowsKv; ++i) {
+    const int r = r0 + i * kv_warps;
+    const __nv_bfloat16* src = r < p.Hkv ? p.k + t * p.k_st + r * p.k_sh : p.v + t * p.v_st + (r - p.Hkv) * p.v_sh;
+    if (r < rows) own[i] = __ldg(reinterpret_cast<const uint4*>(src + 8 * lane));
+  }
+  if (bad) {
+    if (r0 == 0 && lane == 0 && p.status != nullptr) atomicOr(p.status, static_cast<int32_t>(kStatusBadPosition));
+    return;
   }
   Angles an;
-  if (p.R > 0) {
-    if (pos < 0 || pos >= p.P) {
-      if (r0 == 0 && lane == 0 && p.status != nullptr) atomicOr(p.status, static_cast<int32_t>(kStatusBadPosition));
-      return;
-    }
-    if (8 * lane < p.R) load_angles(p, pos, lane, an);
-  }
+  if (8 * lane < p.R) load_angles(p, pos, lane, an);
   const bool put = slot >= 0 && slot < p.S;
   if (slot >= p.S && r0 == 0 && lane == 0 && p.status != nullptr)
     atomicOr(p.status, static_cast<int32_t>(kStatusOobSlot));
-  __syncwarp();
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int r = r0 + i * static_cast<int>(per_tok);
+  for (int i = 0; i < kRowsKv; ++i) {
+    const int r = r0 + i * kv_warps;
     if (r >= rows) break;
-    if (r < p.Hq) {
-      __nv_bfloat16* dst = p.q_out + t * p.qo_st + r * p.qo_sh;
-      float y[8];
-      rotate8(p, own[i], an, lane, y);
-      if (8 * lane < p.R || p.q_out != p.q)
-        *reinterpret_cast<uint4*>(dst + 8 * lane) = 8 * lane < p.R ? pack8(y) : own[i];
-      continue;
-    }
-    const int kv = r - p.Hq >= p.Hkv ? 1 : 0;             // K rows, then V rows
-    const int g = r - p.Hq - kv * p.Hkv;
+    const int kv = r >= p.Hkv ? 1 : 0;                    // K rows, then V rows
+    const int g = r - kv * p.Hkv;
     char* row = p.cache[kv] + static_cast<int64_t>(put ? slot : 0) * p.c_ss + g * p.c_sh;
     __nv_bfloat16* seen = p.seen[kv] == nullptr ? nullptr : p.seen[kv] + (t * p.Hkv + g) * 256 + 8 * lane;
     if constexpr (kFormat == kE2m1) {

@@ -116,7 +116,8 @@ qsa_status_t run(const qsa_append_shape_t* s, AppendParams& p, void* stream) {
     const volatile float six = 6.f * p.ts[i];           // FP32, rounded, on every host
     p.inv[i] = 1.f / six;
   }
-  const int64_t warps = p.T * ((p.Hq + 2LL * p.Hkv + qsa::ap::kRows - 1) / qsa::ap::kRows);
+  const int64_t warps = p.T * ((p.Hq + qsa::ap::kRowsQ - 1) / qsa::ap::kRowsQ +
+                               (2LL * p.Hkv + qsa::ap::kRowsKv - 1) / qsa::ap::kRowsKv);
   const unsigned grid = static_cast<unsigned>((warps + qsa::ap::kWarps - 1) / qsa::ap::kWarps);
   qsa::ap::qsa_append_kernel<kFormat><<<grid, 32 * qsa::ap::kWarps, 0, static_cast<cudaStream_t>(stream)>>>(p);
   return cudaGetLastError() == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
