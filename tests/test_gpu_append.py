@@ -148,6 +148,24 @@ def test_formats(C, fmt, heads, rot, inter, T):
     check(fmt, cache, before, q_out, (ks, vs), q, k, v, table, pos, slots, rot, inter, S)
 
 
+@pytest.mark.parametrize("heads,rot,inter", [((9, 2), 80, False), ((17, 1), 256, False), ((41, 7), 112, True),
+                                             ((8, 4), 0, False), ((25, 5), 256, True)])
+def test_shares_of_the_warps(C, heads, rot, inter):
+    """Head counts that do not divide into a warp's rows, rotary widths that are not powers of two."""
+    S, T = 64, 11
+    q, k, v, table, pos, slots = case(C, T, heads, max(rot, 2), S, seed=rot + heads[0])
+    if rot == 0:
+        table, pos = None, None
+    cache = new_cache(C, "bf16", S, heads[1])
+    before = clone(cache)
+    q_out, _, _ = call(C, "bf16", cache, k, v, pos, slots, table, q=q, interleaved=inter)
+    torch.cuda.synchronize()
+    check("bf16", cache, before, q_out, (None, None), q, k, v, table, pos, slots, rot, inter, S)
+    got = C.kv_append(k, v, pos, slots, table, *cache, q=q, q_out=q, interleaved=inter)
+    torch.cuda.synchronize()
+    assert torch.equal(got, q_out)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_padding_bad_slots_and_positions(C, fmt):
     T, S = 40, 77
