@@ -171,6 +171,23 @@ def test_warps_per_unit(C, heads, T):
     assert compare(out[ti], lse[ti], reference(q, cache, ks, vs, idx, nv, tokens=t), f"T={T}") >= heads[0]
 
 
+@pytest.mark.parametrize("heads", [(12, 1), (6, 1)])
+@pytest.mark.parametrize("T,K", [(1200, 200), (1900, 200), (500, 30), (140, 40)])
+def test_warps_per_short_unit(C, heads, T, K):
+    """Short lists: one warp to a unit in one round and in two, and several warps with a group or two between them."""
+    S = 500
+    q, cache, ks, vs, g = case(C, T, S, heads, seed=T + K)
+    idx = W.random_lists(T, 1, K, S, g, DEV)
+    nv = torch.randint(0, K + 1, (T, 1), generator=g, device=DEV, dtype=torch.int32)
+    nv[::5] = K
+    nv[3] = 0
+    out, lse = C.sparse_prefill_fp4_fwd(q, cache, idx, ks, vs, n_valid=nv)
+    torch.cuda.synchronize()
+    t = sorted({0, 1, 2, 3, T - 2, T - 1, *range(0, T, 29)})
+    ti = torch.tensor(t)
+    assert compare(out[ti], lse[ti], reference(q, cache, ks, vs, idx, nv, tokens=t), f"T={T}") >= heads[0]
+
+
 def test_two_streams_at_once(C):
     """Appends and decodes of two batches on two streams, as when each runs alone."""
     runs = []

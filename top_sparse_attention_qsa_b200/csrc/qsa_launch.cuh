@@ -222,24 +222,36 @@ cudaError_t launch_f4_with(const qsa::f4::F4Params& fp, int64_t units, cudaStrea
   return launch_f4_kernel(qsa_attn_f4_kernel<kBlocks, W>, kThreads4, H_SMEM, done[0], fp, units, stream);
 }
 
-// Warps per unit: the count whose slowest warp takes the fewest groups of 32
-// keys, counting what a unit costs beside its keys as 2 groups (Q and the
-// output; 4 with the merge of several warps).
+// Warps per unit: the count with the least time by a model fitted to all four
+// counts over 1 to 2368 units of 1 to 64 groups of 32 keys.  In units of the
+// time a group takes with every warp of the SM at work, a unit costs its
+// slowest warp's groups and `fixed` (Q, output, merge); with at most 4 warps of
+// an SM at work, one to a scheduler, all of it takes `alone` of that, and more
+// in proportion up to all of them.  Units run in rounds over the SMs' slots, the
+// last one as full as it is.  Measured, us (148 units, heads (24,2)): one group
+// 7.5, 7.8, 6.4, 7.1 with 1, 2, 4, 8 warps to a unit; two groups 9.0, 7.8, 6.5,
+// 7.1; 64 groups 101, 55, 31.5, 26.7; 1184 units of 64 groups 155, 166, 178, 195.
 template <bool kBlocks>
 cudaError_t launch_f4(const qsa::f4::F4Params& fp, cudaStream_t stream) {
   const int64_t units = fp.t.T * fp.t.Hkv * fp.t.splits;
   const int nsm = sm_count();
   if (nsm <= 0) return cudaErrorInvalidDevice;
-  const int warps = fp.t.G <= 8 ? qsa::f4::kWarpsN : qsa::f4::kWarps4;
+  const bool narrow = fp.t.G <= 8;
+  const int warps = narrow ? qsa::f4::kWarpsN : qsa::f4::kWarps4;
+  static constexpr double kFixed[2][4] = {{3.1, 2.5, 2.0, 1.7}, {2.0, 2.1, 1.5, 0.9}};
+  const double alone = narrow ? 0.55 : 0.7;
   const int64_t groups = (fp.t.chunk + qsa::f4::kGroup - 1) / qsa::f4::kGroup;
   int best = 1;
-  int64_t best_cost = 0;
-  for (int w0 = 1; w0 <= 8; w0 *= 2) {
-    const int w = w0 == 8 ? warps : w0;
-    const int64_t slots = static_cast<int64_t>(nsm) * (warps / w);
-    const int64_t cost = ((units + slots - 1) / slots) * ((groups + w - 1) / w + (w == 1 ? 2 : 4));
-    if (w == 1 || cost < best_cost) {
-      best = w0;
+  double best_cost = 0.;
+  for (int i = 0; i < 4; ++i) {
+    const int w = i == 3 ? warps : 1 << i;
+    const int64_t slots = static_cast<int64_t>(nsm) * (warps / w), rest = units % slots;
+    const int64_t busy = (rest + nsm - 1) / nsm * w;    // warps at work on an SM in the last round
+    const double last = rest == 0 ? 0. : busy <= 4 ? alone : alone + (1. - alone) * (busy - 4) / (warps - 4);
+    const double cost = (static_cast<double>(units / slots) + last) *
+                        (kFixed[narrow][i] + static_cast<double>((groups + w - 1) / w));
+    if (i == 0 || cost < best_cost) {
+      best = 1 << i;
       best_cost = cost;
     }
   }
