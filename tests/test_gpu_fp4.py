@@ -365,6 +365,27 @@ def test_workspace_belongs_to_the_launching_stream(C):
     assert torch.equal(out, want) and torch.equal(lse, wl)
 
 
+def test_allocated_workspace_in_a_graph(C):
+    """A captured call that allocates its workspace and outputs: replays give what an eager call gives."""
+    heads, T, ctx, K = (24, 2), 40, 400, 380
+    q, cache, ks, vs, g = case(C, T, T * ctx, heads, seed=64)
+    base = (torch.arange(T, dtype=torch.int32, device=DEV) * ctx).view(T, 1, 1)
+    lists = [W.random_lists(T, 2, K, ctx, g, DEV) + base for _ in "ab"]
+    assert C.decode_fp4_workspace_bytes(q, cache, lists[0], 3) > 0
+    call = lambda idx: C.sparse_decode_fp4_fwd(q, cache, idx, ks, vs, num_splits=3)
+    want = [call(idx) for idx in lists]
+    idx = lists[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = call(idx)
+    for i in (1, 0):
+        idx.copy_(lists[i])
+        junk = torch.full((1 << 22,), float("nan"), device=DEV)  # eager memory between the replays
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1]) and bool(junk.isnan().all())
+
+
 def test_signs_repeats_and_ranges(C):
     """Negative tensor scales, a row named more than once, and integers past 32 bits."""
     T, S, heads = 5, 400, (24, 2)
