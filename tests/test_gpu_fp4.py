@@ -345,6 +345,24 @@ def test_split_k_decode(C, heads, T, splits):
     assert torch.equal(again, out)
 
 
+@pytest.mark.parametrize("heads", [(24, 2), (16, 2)])
+@pytest.mark.parametrize("T,K", [(1, 256), (3, 257), (16, 384), (24, 384), (24, 512), (40, 500), (8, 2048), (24, 1024)])
+def test_automatic_chunks(C, heads, T, K):
+    """The chunks that are picked for short and long lists, with and without room for clusters."""
+    ctx = K + 52
+    q, cache, ks, vs, g = case(C, T, T * ctx, heads, seed=T + K)
+    idx = W.random_lists(T, 2, K, ctx, g, DEV) + (torch.arange(T, dtype=torch.int32, device=DEV) * ctx).view(T, 1, 1)
+    nv = torch.full((T, 2), K, dtype=torch.int32, device=DEV)
+    nv[T // 2, 0], nv[T - 1, 1] = 130, 0
+    need = C.decode_fp4_workspace_bytes(q, cache, idx)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV) if need else None
+    out, lse = C.sparse_decode_fp4_fwd(q, cache, idx, ks, vs, n_valid=nv, workspace=ws)
+    torch.cuda.synchronize()
+    t = sorted({0, T // 2, T - 1})
+    ti = torch.tensor(t)
+    assert compare(out[ti], lse[ti], reference(q, cache, ks, vs, idx, nv, tokens=t), f"T={T} K={K}") == heads[0] // 2
+
+
 def test_workspace_belongs_to_the_launching_stream(C):
     """An allocated workspace is let go on return, with its kernels still to run:
     only work of the same stream may be given its memory."""

@@ -340,19 +340,28 @@ struct Cache4 {
 
 // The chunks of a decode over a 4-bit cache, and whether those of each list run
 // as one cluster (which needs no workspace).  Where the automatic count does
-// not fit as resident clusters, one of up to a quarter fewer that does is
-// taken: 17 tokens, (16,2), 1024 entries take 9.7 us in clusters of 3 and 9.8
-// as 4 chunks and a merge, which is a launch and a workspace more.
+// not fit as resident clusters, the largest smaller one that does is taken if
+// its slowest warp has no more groups of 32 keys: 24 tokens, (24,2), 1024
+// entries take 12.4 us in clusters of 2 and 13.5 as 3 chunks and a merge launch;
+// 8 tokens, 2048 entries, with a second group to the warps, 12.4 in clusters of
+// 6 and 11.1 as 8 chunks and a merge.  Lists of 257 to 512 entries are cut into
+// chunks of 128 where these fit: 384 entries take 8.0 us (10.3 uncut), 512 8.2
+// (8.9 in two).  256 and fewer gain nothing, longer ones less than the larger
+// clusters cost.
 bool plan_f4(const qsa_shape_t* s, int32_t num_splits, SplitPlan* pl, bool* cluster) {
   *cluster = false;
   if (!plan_splits(s, num_splits, pl)) return false;
   const int G = s->num_q_heads / s->num_kv_heads;
   const int64_t lists = s->num_tokens * s->num_kv_heads;
-  const int32_t most = pl->splits;
-  for (int32_t n = most; n >= 2 && n >= (num_splits > 0 ? most : most - most / 4); --n) {
+  const int64_t step = static_cast<int64_t>(qsa::f4::kGroup) * (G <= 8 ? qsa::f4::kWarpsN : qsa::f4::kWarps4);
+  const auto groups = [step](const SplitPlan& p) { return (p.chunk + step - 1) / step; };   // of the slowest warp
+  const int64_t most = groups(*pl);
+  const bool given = num_splits > 0;
+  const int32_t first = !given && s->topk > 256 && s->topk <= 512 ? 4 : pl->splits;
+  for (int32_t n = first; n >= 2 && (n == first || !given); --n) {
     SplitPlan p;
     if (!plan_splits(s, n, &p)) return false;
-    if (f4_cluster_fits(G, lists, p.splits)) {
+    if (groups(p) <= most && f4_cluster_fits(G, lists, p.splits)) {
       *pl = p;
       *cluster = true;
       break;
