@@ -596,10 +596,15 @@ qsa_status_t qsa_sparse_prefill_fp4_fwd(
  * log-sum-exp merge, with the chunks computed by the kernel of
  * qsa_sparse_prefill_fp4_fwd over token lists.  Where the 2 to 8 chunks of
  * every list fit on the device as resident clusters, they run and merge in
- * one launch and need no workspace; otherwise the partial results go to
+ * one launch and use no workspace; otherwise the partial results go to
  * `workspace` as in qsa_sparse_decode_fwd.
- * qsa_sparse_decode_fp4_workspace_bytes says how many bytes that is for this
- * shape, num_splits and the current device (0: `workspace` may be NULL).
+ * qsa_sparse_decode_fp4_workspace_bytes says how many bytes to provide:
+ *  - num_splits <= 0: what this shape needs on the current device, 0 where
+ *    clusters serve it (`workspace` may then be NULL).
+ *  - num_splits > 0: what the partial results of that count take, on every
+ *    device.  A workspace that is named for such a call (`workspace` not NULL
+ *    or workspace_bytes not 0) is checked against it also where clusters leave
+ *    it alone; NULL with 0 bytes is taken there and is QSA_ERR_NULL elsewhere.
  */
 size_t qsa_sparse_decode_fp4_workspace_bytes(const qsa_shape_t* shape,
                                              int32_t num_splits);

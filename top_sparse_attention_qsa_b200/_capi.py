@@ -804,8 +804,9 @@ def sparse_prefill_fp4_fwd(q, cache: Fp4Cache, topk_idx, k_scale: float, v_scale
 
 
 def decode_fp4_workspace_bytes(q, cache: Fp4Cache, topk_idx, num_splits: int = 0) -> int:
-    """Scratch bytes sparse_decode_fp4_fwd needs on q's device: 0 for a single
-    chunk, and for chunks that run as one cluster."""
+    """Scratch bytes to give sparse_decode_fp4_fwd on q's device: 0 for a single
+    chunk and, with the automatic count, for chunks that run as one cluster; for
+    a given count above one, what its partial results take on any device."""
     shape = make_shape(q, cache.buffer, topk_idx, q)
     with torch.cuda.device(q.device):
         return int(_lib.qsa_sparse_decode_fp4_workspace_bytes(ctypes.byref(shape), int(num_splits)))

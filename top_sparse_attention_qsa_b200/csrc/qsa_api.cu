@@ -398,7 +398,11 @@ qsa_status_t run_f4(const qsa_shape_t* s, int32_t block_size, const int32_t* las
   const bool split = decode && pl.splits > 1;
   // units are counted in 32 bits, one grid past the end included
   if (s->num_tokens * s->num_kv_heads > (0x7fffffffLL - 65536) / (split ? pl.splits : 1)) return QSA_ERR_UNSUPPORTED;
-  if (split && !cluster) {
+  // A workspace that is named for a given chunk count is checked against that
+  // count also where the chunks run as clusters and leave it alone: what is
+  // refused then is the same on every device.
+  const bool named = num_splits > 0 && (workspace != nullptr || workspace_bytes != 0);
+  if (split && (!cluster || named)) {
     if (workspace == nullptr) return QSA_ERR_NULL;
     if (workspace_bytes < pl.total_bytes) return QSA_ERR_SHAPE;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return QSA_ERR_ALIGN;
@@ -647,7 +651,7 @@ size_t qsa_sparse_decode_fp4_workspace_bytes(const qsa_shape_t* shape, int32_t n
     return 0;
   SplitPlan pl;
   bool cluster = false;
-  if (!plan_f4(shape, num_splits, &pl, &cluster) || pl.splits <= 1 || cluster) return 0;
+  if (!plan_f4(shape, num_splits, &pl, &cluster) || pl.splits <= 1 || (cluster && num_splits <= 0)) return 0;
   return pl.total_bytes;
 }
 

@@ -328,19 +328,22 @@ PyObject* sparse_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
         ws = THPVariable_Unpack(a[11]);
         need(ws.is_cuda() && ws.get_device() == dev && ws.is_contiguous(), "workspace must be a contiguous CUDA tensor");
         bytes = ws.numel() * ws.element_size();
-      } else {
-        bytes = qsa_sparse_decode_fp4_workspace_bytes(&s, splits);
-        if (bytes > 0) {
-          // owned by the launching stream: it is let go on return, before the
-          // kernels have run
-          const c10::cuda::CUDAStreamGuard own(
-              c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), static_cast<c10::DeviceIndex>(dev)));
-          ws = fresh({static_cast<int64_t>(bytes)}, at::kByte, dev);
-        }
       }
-      rc = qsa_sparse_decode_fp4_fwd(&s, q.data_ptr(), c, c + 256, c + 128, c + 272, buf.stride(0), buf.stride(1), list,
-                                     n_valid, scale, ks, vs, out.data_ptr(), lp, status, splits,
-                                     ws.defined() ? ws.data_ptr() : nullptr, bytes, stream);
+      auto call = [&] {
+        return qsa_sparse_decode_fp4_fwd(&s, q.data_ptr(), c, c + 256, c + 128, c + 272, buf.stride(0), buf.stride(1),
+                                         list, n_valid, scale, ks, vs, out.data_ptr(), lp, status, splits,
+                                         ws.defined() ? ws.data_ptr() : nullptr, bytes, stream);
+      };
+      rc = call();
+      // refused for want of a workspace, where no cluster serves the call
+      if (rc == QSA_ERR_NULL && !given(a[11]) && (bytes = qsa_sparse_decode_fp4_workspace_bytes(&s, splits)) > 0) {
+        // owned by the launching stream: it is let go on return, before the
+        // kernels have run
+        const c10::cuda::CUDAStreamGuard own(
+            c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), static_cast<c10::DeviceIndex>(dev)));
+        ws = fresh({static_cast<int64_t>(bytes)}, at::kByte, dev);
+        rc = call();
+      }
     } else {
       rc = qsa_sparse_prefill_fp4_fwd(&s, integer32(a[8], "block_size"), last, q.data_ptr(), c, c + 256, c + 128,
                                       c + 272, buf.stride(0), buf.stride(1), list, n_valid, scale, ks, vs,
