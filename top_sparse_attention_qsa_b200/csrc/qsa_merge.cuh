@@ -9,7 +9,8 @@
 // for QSA named on page "Qwen4-Exp QSA llega al Ascend de Huawei", section
 // "Dónde encaja esto en el despliegue del servicio de Qwen4Exp" (vLLM #59279);
 // a chunk with no live entry has lse_s = -inf and weight 0, and a row whose
-// chunks are all empty gets out = +0.0 and lse = -inf.
+// chunks are all empty gets out = +0.0 and lse = -inf.  A chunk with lse_s = NaN
+// (a NaN score) makes the row NaN, in out and lse.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -34,14 +35,18 @@ __global__ void __launch_bounds__(64) qsa_merge_splits_kernel(const MergeParams 
   if (r >= p.rows) return;
   const float* pl = p.part_lse + r * p.splits;
   float m = -INFINITY;
-  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, pl[s]);
+  bool nan = false;                     // (fmaxf passes over NaN)
+  for (int s = 0; s < p.splits; ++s) {
+    m = fmaxf(m, pl[s]);
+    nan |= pl[s] != pl[s];
+  }
   const int64_t t = r / p.Hq;
   const int h = static_cast<int>(r - t * p.Hq);
   __nv_bfloat16* orow = p.out + t * p.o_st + static_cast<int64_t>(h) * p.o_sh;
   const int d = 4 * threadIdx.x;
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   float wsum = 0.f;
-  if (m != -INFINITY) {
+  if (m != -INFINITY || nan) {
     for (int s = 0; s < p.splits; ++s) {
       const float w = expf(pl[s] - m);  // 0 for an empty chunk
       wsum += w;
@@ -52,7 +57,8 @@ __global__ void __launch_bounds__(64) qsa_merge_splits_kernel(const MergeParams 
       acc[3] += w * o.w;
     }
   }
-  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+  // wsum = 0: no chunk has a key; a NaN stays NaN
+  const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
   __nv_bfloat162 a = __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv);
   __nv_bfloat162 b = __floats2bfloat162_rn(acc[2] * inv, acc[3] * inv);
   uint2 pk;
@@ -60,7 +66,7 @@ __global__ void __launch_bounds__(64) qsa_merge_splits_kernel(const MergeParams 
   pk.y = *reinterpret_cast<uint32_t*>(&b);
   *reinterpret_cast<uint2*>(orow + d) = pk;
   if (p.lse != nullptr && threadIdx.x == 0)
-    p.lse[t * p.lse_st + h] = wsum > 0.f ? m + logf(wsum) : -INFINITY;
+    p.lse[t * p.lse_st + h] = wsum == 0.f ? -INFINITY : m + logf(wsum);
 }
 
 }  // namespace qsa
