@@ -1,0 +1,89 @@
+"""Calls on a stream that is not the current one, on two streams at once, and
+beside other Python threads."""
+import pytest
+import torch
+
+from test_gpu_fp4 import case
+from top_sparse_attention_qsa_b200 import workloads as W
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
+
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def C():
+    from top_sparse_attention_qsa_b200 import _capi
+    return _capi
+
+
+def calls(C):
+    """Every call that makes its own outputs, as f(stream) -> tuple of tensors."""
+    T, S, heads, K = 40, 8000, (24, 2), 650
+    q, cache, ks, vs, g = case(C, T, S, heads, seed=95)
+    idx = W.random_lists(T, 2, K, S, g, DEV)
+    blocks = W.random_lists(T, 2, 64, S // 4, g, DEV)
+    k, v = (torch.randn((T, 2, 256), generator=g, device=DEV).to(torch.bfloat16) for _ in "kv")
+    pos = torch.arange(T, dtype=torch.int32, device=DEV)
+    table = C.rope_table(S, 64, device=DEV)
+    kc, vc = (torch.randn((S, 2, 256), generator=g, device=DEV).to(torch.bfloat16) for _ in "kv")
+    k8, v8 = kc.to(torch.float8_e4m3fn), vc.to(torch.float8_e4m3fn)
+    spare = [x.clone() for x in (kc, vc, k8, v8, cache.buffer)]
+    qi = torch.randn((T, 4, 128), generator=g, device=DEV).to(torch.bfloat16)
+    ki = torch.randn((S // 4, 128), generator=g, device=DEV).to(torch.bfloat16)
+    last, first = torch.full((T,), S - 1, dtype=torch.int32, device=DEV), torch.zeros((T,), dtype=torch.int32, device=DEV)
+    scores = C.indexer_scores(qi, ki, last, first)
+    torch.cuda.synchronize()
+    return {
+        "kv_append": lambda s: (C.kv_append(k, v, pos, pos, table, spare[0], spare[1], q=q, stream=s),),
+        "kv_append_fp8": lambda s: C.kv_append_fp8(k, v, pos, pos, table, spare[2], spare[3], 0.02, 0.02, q=q,
+                                                   want_seen=True, stream=s),
+        "kv_append_fp4": lambda s: C.kv_append_fp4(k, v, pos, pos, table, C.Fp4Cache(spare[4]), ks, vs, q=q,
+                                                   want_seen=True, stream=s),
+        "prefill_fp4": lambda s: C.sparse_prefill_fp4_fwd(q, cache, idx, ks, vs, stream=s),
+        "decode_fp4": lambda s: C.sparse_decode_fp4_fwd(q, cache, idx, ks, vs, stream=s),
+        "decode_fp4 workspace": lambda s: C.sparse_decode_fp4_fwd(q, cache, idx, ks, vs, num_splits=3, stream=s),
+        "prefill": lambda s: C.sparse_prefill_fwd(q, kc, vc, idx, stream=s),
+        "debug_gather": lambda s: C.sparse_prefill_debug_gather(q, kc, vc, idx, stream=s),
+        "block": lambda s: C.sparse_prefill_block_fwd(q, kc, vc, blocks, 4, stream=s),
+        "prefill_fp8": lambda s: C.sparse_prefill_fp8_fwd(q, k8, v8, idx, stream=s),
+        "debug_gather_lists": lambda s: C.sparse_prefill_debug_gather_lists(q, kc, vc, blocks, 4, stream=s),
+        "decode": lambda s: C.sparse_decode_fwd(q, kc, vc, idx, num_splits=3, stream=s),
+        "decode_fp8": lambda s: C.sparse_decode_fp8_fwd(q, k8, v8, idx, num_splits=3, stream=s),
+        "fold_heads": lambda s: (C.indexer_fold_heads(qi, ki, stream=s),),
+        "scores": lambda s: (C.indexer_scores(qi, ki, last, first, stream=s),),
+        "scores unfolded": lambda s: (C.indexer_scores(qi, ki, last, first, fold=False, stream=s),),
+        "topk": lambda s: C.topk_select(scores, last, first, S // 4, 64, copies=2, stream=s),
+        "select": lambda s: C.indexer_select(qi, ki, last, first, 64, stream=s),
+    }
+
+
+NEW = ("kv_append", "kv_append_fp8", "kv_append_fp4", "prefill_fp4", "decode_fp4", "decode_fp4 workspace")
+
+
+def outputs_belong_to_the_launching_stream(run):
+    """Outputs made for a call on another stream are that stream's: once dropped,
+    their memory is not given to work of the current stream."""
+    want = run(None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = run(side.cuda_stream)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    del want
+    spans = [(x.data_ptr(), x.data_ptr() + x.untyped_storage().nbytes()) for x in got]
+    sizes = [x.untyped_storage().nbytes() for x in got]
+    del got, a, b
+    later = [torch.empty(n, dtype=torch.uint8, device=DEV) for n in sizes for _ in range(4)]
+    for x in later:
+        for lo, hi in spans:
+            assert x.data_ptr() + x.numel() <= lo or x.data_ptr() >= hi
+
+
+def test_outputs_of_cache_and_4bit_calls(C):
+    every = calls(C)
+    for name in NEW:
+        outputs_belong_to_the_launching_stream(every[name])

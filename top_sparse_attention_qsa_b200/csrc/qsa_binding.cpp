@@ -88,14 +88,30 @@ int32_t size32(int64_t n) {
   return static_cast<int32_t>(n);
 }
 
-void* stream_of(PyObject* o, int dev) {
-  if (given(o)) {
-    void* s = PyLong_AsVoidPtr(o);
-    if (s == nullptr && PyErr_Occurred()) throw python_error();
-    return s;
+// The stream of a call, current for its time: what the call makes (outputs, a
+// workspace that is let go on return with its kernels still to run) then
+// belongs to the stream that writes it, and once dropped goes to no work of
+// another.
+class Launch {
+ public:
+  Launch(PyObject* o, int dev) {
+    const auto d = static_cast<c10::DeviceIndex>(dev);
+    if (given(o)) {
+      stream_ = PyLong_AsVoidPtr(o);
+      if (stream_ == nullptr && PyErr_Occurred()) throw python_error();
+      on_stream_.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream_), d));
+    } else {
+      stream_ = c10::cuda::getCurrentCUDAStream(d).stream();
+      if (d != c10::cuda::current_device()) on_device_.set_index(d);
+    }
   }
-  return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
-}
+  void* stream() const { return stream_; }
+
+ private:
+  void* stream_ = nullptr;
+  c10::cuda::OptionalCUDAStreamGuard on_stream_;
+  c10::cuda::OptionalCUDAGuard on_device_;
+};
 
 // An output on CUDA device `dev`, past the dispatcher: an enqueue with three
 // outputs takes 10.5 us instead of 11.6, with one 5.3 instead of 5.7.
@@ -157,6 +173,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto dt = format == 0 ? at::kBFloat16 : format == 1 ? at::kFloat8_e4m3fn : at::kByte;
     const Tensor& k = tensor(a[1], "k", at::kBFloat16, -1);
     const int dev = k.get_device();
+    const Launch at(a[17], dev);
     const Tensor& v = tensor(a[2], "v", at::kBFloat16, dev);
     need(k.dim() == 3 && v.sizes() == k.sizes(), "k and v must be [T, Hkv, 256]");
     const Tensor& kc = tensor(a[6], format == 2 ? "cache" : "k_cache", dt, dev);
@@ -225,9 +242,6 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       }
     }
     int32_t* status = status_word(a[16], dev);
-    void* stream = stream_of(a[17], dev);
-    const c10::cuda::OptionalCUDAGuard on(dev == c10::cuda::current_device() ? std::nullopt
-                                                                             : std::optional<c10::Device>(k.device()));
     void* qi = ptr(a[10]);
     void* qo = q_out.has_value() ? q_out->data_ptr() : nullptr;
     void* ks = seen[0].has_value() ? seen[0]->data_ptr() : nullptr;
@@ -235,17 +249,17 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     char* c = static_cast<char*>(kc.data_ptr());
     qsa_status_t rc;
     if (format == 0) {
-      rc = qsa_kv_append(&s, qi, qo, k.data_ptr(), v.data_ptr(), table, positions, slots, c, ptr(a[7]), status, stream);
+      rc = qsa_kv_append(&s, qi, qo, k.data_ptr(), v.data_ptr(), table, positions, slots, c, ptr(a[7]), status, at.stream());
     } else if (format == 1) {
       rc = qsa_kv_append_fp8(&s, qi, qo, k.data_ptr(), v.data_ptr(), table, positions, slots,
                              static_cast<float>(number(a[8])), static_cast<float>(number(a[9])), c, ptr(a[7]), ks, vs,
-                             status, stream);
+                             status, at.stream());
     } else {
       s.bscale_stride_slot = s.kv_stride_slot;
       s.bscale_stride_head = s.kv_stride_head;
       rc = qsa_kv_append_fp4(&s, qi, qo, k.data_ptr(), v.data_ptr(), table, positions, slots,
                              static_cast<float>(number(a[8])), static_cast<float>(number(a[9])), c, c + 256, c + 128,
-                             c + 272, ks, vs, status, stream);
+                             c + 272, ks, vs, status, at.stream());
     }
     return result(rc, q_out, seen[0], seen[1]);
   });
@@ -261,6 +275,7 @@ PyObject* sparse_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const bool decode = integer(a[0]) != 0;
     const Tensor& q = tensor(a[1], "q", at::kBFloat16, -1);
     const int dev = q.get_device();
+    const Launch at(a[15], dev);
     const Tensor& buf = tensor(a[2], "cache", at::kByte, dev);
     const Tensor& idx = tensor(a[3], "topk_idx", at::kInt, dev);
     need(q.dim() == 3 && idx.dim() == 3 && buf.dim() == 3, "q, the cache and topk_idx must be 3-d");
@@ -310,9 +325,6 @@ PyObject* sparse_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     s.o_stride_tok = out.stride(0);
     s.o_stride_head = out.stride(1);
     int32_t* status = status_word(a[14], dev);
-    void* stream = stream_of(a[15], dev);
-    const c10::cuda::OptionalCUDAGuard on(dev == c10::cuda::current_device() ? std::nullopt
-                                                                             : std::optional<c10::Device>(q.device()));
     const char* c = static_cast<const char*>(buf.data_ptr());
     const int32_t* list = static_cast<const int32_t*>(idx.data_ptr());
     float* lp = lse.has_value() ? static_cast<float*>(lse->data_ptr()) : nullptr;
@@ -332,22 +344,18 @@ PyObject* sparse_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
       auto call = [&] {
         return qsa_sparse_decode_fp4_fwd(&s, q.data_ptr(), c, c + 256, c + 128, c + 272, buf.stride(0), buf.stride(1),
                                          list, n_valid, scale, ks, vs, out.data_ptr(), lp, status, splits,
-                                         ws.defined() ? ws.data_ptr() : nullptr, bytes, stream);
+                                         ws.defined() ? ws.data_ptr() : nullptr, bytes, at.stream());
       };
       rc = call();
       // refused for want of a workspace, where no cluster serves the call
       if (rc == QSA_ERR_NULL && !given(a[11]) && (bytes = qsa_sparse_decode_fp4_workspace_bytes(&s, splits)) > 0) {
-        // owned by the launching stream: it is let go on return, before the
-        // kernels have run
-        const c10::cuda::CUDAStreamGuard own(
-            c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), static_cast<c10::DeviceIndex>(dev)));
         ws = fresh({static_cast<int64_t>(bytes)}, at::kByte, dev);
         rc = call();
       }
     } else {
       rc = qsa_sparse_prefill_fp4_fwd(&s, integer32(a[8], "block_size"), last, q.data_ptr(), c, c + 256, c + 128,
                                       c + 272, buf.stride(0), buf.stride(1), list, n_valid, scale, ks, vs,
-                                      out.data_ptr(), lp, status, stream);
+                                      out.data_ptr(), lp, status, at.stream());
     }
     return result(rc, std::optional<Tensor>(out), lse);
   });
