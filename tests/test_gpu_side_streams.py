@@ -1,5 +1,7 @@
 """Calls on a stream that is not the current one, on two streams at once, and
 beside other Python threads."""
+import ctypes
+
 import pytest
 import torch
 
@@ -87,3 +89,24 @@ def test_outputs_of_cache_and_4bit_calls(C):
     every = calls(C)
     for name in NEW:
         outputs_belong_to_the_launching_stream(every[name])
+
+
+def test_outputs_of_the_other_calls(C):
+    every = calls(C)
+    for name in every:
+        if name not in NEW:
+            outputs_belong_to_the_launching_stream(every[name])
+
+
+def test_forms_of_a_stream_handle(C):
+    """The default stream's handle 0, a stream object and a ctypes pointer name a stream as an int does."""
+    every = calls(C)
+    side = torch.cuda.Stream()
+    for name in ("decode", "scores"):
+        want = every[name](None)
+        torch.cuda.synchronize()
+        for s in (0, side, ctypes.c_void_p(side.cuda_stream), ctypes.c_void_p(0)):
+            got = every[name](s)
+            torch.cuda.synchronize()
+            for a, b in zip(got, want):
+                assert torch.equal(a, b)

@@ -3,6 +3,10 @@
 Argument marshalling only: tensors become pointers, sizes and strides; every
 step of the computation runs in the library's CUDA kernels.  Importing this
 module fails loudly when libqsa.so has not been built; there is no fallback.
+
+`stream` of a call is a CUDA stream handle (an int; None: the current stream of
+the tensors' device).  What a call makes itself, outputs and workspaces, belongs
+to that stream.
 """
 from __future__ import annotations
 
@@ -202,6 +206,20 @@ def _need(x: torch.Tensor, name: str, dtype, device=None, host=False):
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
 
 
+def _fresh(shape, dtype, dev, stream, fill=None):
+    """An output or a workspace that a call makes: it belongs to the stream the
+    call runs on (and is filled there), so that its memory, once dropped, goes
+    to no work of another stream while kernels still write it."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):    # a handle: an int or a ctypes.c_void_p
+            stream = torch.cuda.ExternalStream(getattr(stream, "value", stream) or 0, dev)
+        with torch.cuda.stream(stream):
+            return _fresh(shape, dtype, dev, None, fill)
+    if fill is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    return torch.full(shape, fill, dtype=dtype, device=dev)
+
+
 def make_shape(q, k_cache, topk_idx, out, lse=None) -> Shape:
     """Shape/stride descriptor of a call (no checks beyond ranks: the library
     validates sizes, strides and alignment itself)."""
@@ -250,10 +268,10 @@ def sparse_prefill_fwd(q, k_cache, v_cache, topk_idx, n_valid=None, scale: float
         if not n_valid.is_contiguous() or tuple(n_valid.shape) != tuple(topk_idx.shape[:2]):
             raise ValueError("n_valid must be a contiguous [T, Hkv] tensor")
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        out = _fresh(q.shape, torch.bfloat16, dev, stream)
     _need(out, "out", torch.bfloat16, dev)
     if lse is None and want_lse:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
+        lse = _fresh(q.shape[:2], torch.float32, dev, stream)
     if lse is not None:
         _need(lse, "lse", torch.float32, dev)
     if status is not None:
@@ -280,9 +298,9 @@ def sparse_prefill_debug_gather(q, k_cache, v_cache, topk_idx, n_valid=None, sca
     _check_kv(k_cache, v_cache)
     if n_valid is not None:
         _need(n_valid, "n_valid", torch.int32, dev)
-    out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
-    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
-    ids = torch.empty(topk_idx.shape, dtype=torch.int32, device=dev)
+    out = _fresh(q.shape, torch.bfloat16, dev, stream)
+    lse = _fresh(q.shape[:2], torch.float32, dev, stream)
+    ids = _fresh(topk_idx.shape, torch.int32, dev, stream)
     shape = make_shape(q, k_cache, topk_idx, out, lse)
     if stream is None:
         stream = torch.cuda.current_stream(dev).cuda_stream
@@ -360,10 +378,10 @@ def sparse_decode_fwd(q, k_cache, v_cache, topk_idx, n_valid=None, scale: float 
         if not n_valid.is_contiguous() or tuple(n_valid.shape) != tuple(topk_idx.shape[:2]):
             raise ValueError("n_valid must be a contiguous [T, Hkv] tensor")
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        out = _fresh(q.shape, torch.bfloat16, dev, stream)
     _need(out, "out", torch.bfloat16, dev)
     if lse is None and want_lse:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
+        lse = _fresh(q.shape[:2], torch.float32, dev, stream)
     if lse is not None:
         _need(lse, "lse", torch.float32, dev)
     if status is not None:
@@ -371,7 +389,7 @@ def sparse_decode_fwd(q, k_cache, v_cache, topk_idx, n_valid=None, scale: float 
     shape = make_shape(q, k_cache, topk_idx, out, lse)
     need = int(_lib.qsa_sparse_decode_workspace_bytes(ctypes.byref(shape), int(num_splits)))
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _fresh(need, torch.uint8, dev, stream)
     ws_bytes = 0
     if workspace is not None:
         _need(workspace, "workspace", workspace.dtype, dev)
@@ -442,10 +460,10 @@ def sparse_prefill_block_fwd(q, k_cache, v_cache, block_idx, block_size: int, la
         if not n_valid.is_contiguous() or tuple(n_valid.shape) != tuple(block_idx.shape[:2]):
             raise ValueError("n_valid must be a contiguous [T, Hkv] tensor")
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        out = _fresh(q.shape, torch.bfloat16, dev, stream)
     _need(out, "out", torch.bfloat16, dev)
     if lse is None and want_lse:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
+        lse = _fresh(q.shape[:2], torch.float32, dev, stream)
     if lse is not None:
         _need(lse, "lse", torch.float32, dev)
     if status is not None:
@@ -481,10 +499,10 @@ def sparse_prefill_fp8_fwd(q, k_cache, v_cache, topk_idx, k_scale: float = 1.0, 
         if not n_valid.is_contiguous() or tuple(n_valid.shape) != tuple(topk_idx.shape[:2]):
             raise ValueError("n_valid must be a contiguous [T, Hkv] tensor")
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        out = _fresh(q.shape, torch.bfloat16, dev, stream)
     _need(out, "out", torch.bfloat16, dev)
     if lse is None and want_lse:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
+        lse = _fresh(q.shape[:2], torch.float32, dev, stream)
     if lse is not None:
         _need(lse, "lse", torch.float32, dev)
     if status is not None:
@@ -522,10 +540,10 @@ def sparse_prefill_debug_gather_lists(q, k_cache, v_cache, topk_idx, block_size:
             raise ValueError("n_valid must be a contiguous [T, Hkv] tensor")
     if status is not None:
         _need(status, "status", torch.int32, dev)
-    out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
-    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
+    out = _fresh(q.shape, torch.bfloat16, dev, stream)
+    lse = _fresh(q.shape[:2], torch.float32, dev, stream)
     T, Hkv, K = topk_idx.shape
-    ids = torch.empty((T, Hkv, K * int(block_size)), dtype=torch.int32, device=dev)
+    ids = _fresh((T, Hkv, K * int(block_size)), torch.int32, dev, stream)
     shape = make_shape(q, k_cache, topk_idx, out, lse)
     if stream is None:
         stream = torch.cuda.current_stream(dev).cuda_stream
@@ -553,10 +571,10 @@ def sparse_decode_fp8_fwd(q, k_cache, v_cache, topk_idx, k_scale: float = 1.0, v
         if not n_valid.is_contiguous() or tuple(n_valid.shape) != tuple(topk_idx.shape[:2]):
             raise ValueError("n_valid must be a contiguous [T, Hkv] tensor")
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        out = _fresh(q.shape, torch.bfloat16, dev, stream)
     _need(out, "out", torch.bfloat16, dev)
     if lse is None and want_lse:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
+        lse = _fresh(q.shape[:2], torch.float32, dev, stream)
     if lse is not None:
         _need(lse, "lse", torch.float32, dev)
     if status is not None:
@@ -564,7 +582,7 @@ def sparse_decode_fp8_fwd(q, k_cache, v_cache, topk_idx, k_scale: float = 1.0, v
     shape = make_shape(q, k_cache, topk_idx, out, lse)
     need = int(_lib.qsa_sparse_decode_workspace_bytes(ctypes.byref(shape), int(num_splits)))
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _fresh(need, torch.uint8, dev, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     if stream is None:
         stream = torch.cuda.current_stream(dev).cuda_stream
@@ -614,7 +632,7 @@ def indexer_fold_heads(q_idx, k_idx, out=None, stream=None):
     _need(q_idx, "q_idx", torch.bfloat16, dev)
     T = q_idx.shape[0]
     if out is None:
-        out = torch.empty((T, 2, q_idx.shape[2]), dtype=torch.bfloat16, device=dev)
+        out = _fresh((T, 2, q_idx.shape[2]), torch.bfloat16, dev, stream)
     _need(out, "q_folded", torch.bfloat16, dev)
     if not out.is_contiguous() or tuple(out.shape) != (T, 2, q_idx.shape[2]):
         raise ValueError("q_folded must be a contiguous [T, 2, Dh] tensor")
@@ -645,7 +663,7 @@ def indexer_scores(q_idx, k_idx, positions, seq_start, block_size: int = 4, scor
     if scores is None:
         # rows padded to a multiple of 4 floats: the selection copies 16-byte spans
         NB = k_idx.shape[0]
-        scores = torch.full((T, (NB + 3) // 4 * 4), float("-inf"), dtype=torch.float32, device=dev)[:, :NB]
+        scores = _fresh((T, (NB + 3) // 4 * 4), torch.float32, dev, stream, fill=float("-inf"))[:, :NB]
     _need(scores, "scores", torch.float32, dev)
     if status is not None:
         _need(status, "status", torch.int32, dev)
@@ -671,12 +689,12 @@ def topk_select(scores, positions, seq_start, num_blocks: int, budget: int, bloc
     _need_tok(seq_start, "seq_start", T, dev)
     width = int(budget) + (1 if append_tail else 0)
     if lists is None:
-        lists = torch.empty((T, width), dtype=torch.int32, device=dev)
+        lists = _fresh((T, width), torch.int32, dev, stream)
     _need(lists, "lists", torch.int32, dev)
     if lists.dim() != 2 or lists.shape[0] != T or lists.shape[1] < width or (width > 1 and lists.stride(1) != 1):
         raise ValueError("lists must be [T, >= width] with unit column stride")
     if n_valid is None:
-        n_valid = torch.empty((T, copies), dtype=torch.int32, device=dev)
+        n_valid = _fresh((T, copies), torch.int32, dev, stream)
     _need(n_valid, "n_valid", torch.int32, dev)
     if not n_valid.is_contiguous() or tuple(n_valid.shape) != (T, copies):
         raise ValueError("n_valid must be a contiguous [T, copies] tensor")
