@@ -1,6 +1,8 @@
 """Calls on a stream that is not the current one, on two streams at once, and
 beside other Python threads."""
 import ctypes
+import threading
+import time
 
 import pytest
 import torch
@@ -110,3 +112,43 @@ def test_forms_of_a_stream_handle(C):
             torch.cuda.synchronize()
             for a, b in zip(got, want):
                 assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("call", ["append", "prefill", "decode"])
+def test_other_threads_run_while_a_launch_waits(C, call):
+    """A launch that waits for room in its stream's queue keeps only its own thread waiting."""
+    T, S = 2, 64
+    q, cache, ks, vs, g = case(C, T, S, (3, 1), seed=96)
+    idx = W.random_lists(T, 1, 8, S, g, DEV)
+    k = torch.zeros((T, 1, 256), dtype=torch.bfloat16, device=DEV)
+    pos = torch.arange(T, dtype=torch.int32, device=DEV)
+    table = C.rope_table(S, 64, device=DEV)
+    out = torch.empty_like(q)
+    run = {"append": lambda: C.kv_append_fp4(k, k, pos, pos, table, cache, ks, vs),
+           "prefill": lambda: C.sparse_prefill_fp4_fwd(q, cache, idx, ks, vs, out=out, want_lse=False),
+           "decode": lambda: C.sparse_decode_fp4_fwd(q, cache, idx, ks, vs, out=out, want_lse=False)}[call]
+    run()
+    torch.cuda.synchronize()
+    ticks, stop = [], threading.Event()
+
+    def tick():
+        while not stop.is_set():
+            ticks.append(time.perf_counter())
+            time.sleep(0.002)
+
+    other = threading.Thread(target=tick)
+    other.start()
+    torch.cuda._sleep(2_000_000_000)                     # about a second of the stream
+    begin, longest = time.perf_counter(), (0.0, 0.0, 0.0)
+    while time.perf_counter() - begin < 3 and longest[0] < 0.2:
+        a = time.perf_counter()
+        run()
+        b = time.perf_counter()
+        longest = max(longest, (b - a, a, b))
+    stop.set()
+    other.join()
+    torch.cuda.synchronize()
+    waited, a, b = longest
+    assert waited >= 0.2, "the queue never filled"
+    during = [t for t in ticks if a <= t <= b]
+    assert len(during) > 0.1 * waited / 0.002, f"{len(during)} ticks in {waited:.2f} s"

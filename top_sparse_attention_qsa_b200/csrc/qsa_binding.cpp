@@ -113,6 +113,21 @@ class Launch {
   c10::cuda::OptionalCUDAGuard on_device_;
 };
 
+// Other Python threads run while a call allocates and launches: an allocation
+// may have to free cached memory, a launch may wait for room in its stream's
+// queue (which a host function of that stream can hold up).  No Python object
+// is touched meanwhile.
+class Unlocked {
+ public:
+  Unlocked() : state_(PyEval_SaveThread()) {}
+  ~Unlocked() { PyEval_RestoreThread(state_); }
+  Unlocked(const Unlocked&) = delete;
+  Unlocked& operator=(const Unlocked&) = delete;
+
+ private:
+  PyThreadState* state_;
+};
+
 // An output on CUDA device `dev`, past the dispatcher: an enqueue with three
 // outputs takes 10.5 us instead of 11.6, with one 5.3 instead of 5.7.
 Tensor fresh(at::IntArrayRef sizes, at::ScalarType dt, int dev) {
@@ -173,7 +188,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto dt = format == 0 ? at::kBFloat16 : format == 1 ? at::kFloat8_e4m3fn : at::kByte;
     const Tensor& k = tensor(a[1], "k", at::kBFloat16, -1);
     const int dev = k.get_device();
-    const Launch at(a[17], dev);
+    const Launch on(a[17], dev);
     const Tensor& v = tensor(a[2], "v", at::kBFloat16, dev);
     need(k.dim() == 3 && v.sizes() == k.sizes(), "k and v must be [T, Hkv, 256]");
     const Tensor& kc = tensor(a[6], format == 2 ? "cache" : "k_cache", dt, dev);
@@ -202,22 +217,19 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       table = static_cast<const float*>(cs.data_ptr());
       if (s.rotary_dim > 0) positions = per_token(a[3], "positions", s.num_tokens, dev);
     }
+    const Tensor* q_in = nullptr;
     std::optional<Tensor> q_out;
     if (given(a[10])) {
-      const Tensor& q = tensor(a[10], "q", at::kBFloat16, dev);
+      const Tensor& q = *(q_in = &tensor(a[10], "q", at::kBFloat16, dev));
       need(q.dim() == 3 && q.size(0) == s.num_tokens && q.size(2) == s.head_dim && q.stride(2) == 1,
            "q must be [T, Hq, 256] with contiguous rows");
       if (given(a[11])) {
         q_out = tensor(a[11], "q_out", at::kBFloat16, dev);
         need(q_out->sizes() == q.sizes() && q_out->stride(2) == 1, "q_out must have q's shape and contiguous rows");
-      } else {
-        q_out = fresh(q.sizes(), at::kBFloat16, dev);
       }
       s.num_q_heads = size32(q.size(1));
       s.q_stride_tok = q.stride(0);
       s.q_stride_head = q.stride(1);
-      s.qo_stride_tok = q_out->stride(0);
-      s.qo_stride_head = q_out->stride(1);
     } else {
       need(!given(a[11]), "q_out needs q");
     }
@@ -237,29 +249,36 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         seen[i] = tensor(a[13 + i], name, at::kBFloat16, dev);
         if (seen[i]->sizes() != k.sizes() || !seen[i]->is_contiguous())
           throw ValueFault(std::string(name) + " must be a contiguous [T, Hkv, 256] tensor");
-      } else if (want) {
-        seen[i] = fresh(k.sizes(), at::kBFloat16, dev);
       }
     }
     int32_t* status = status_word(a[16], dev);
-    void* qi = ptr(a[10]);
-    void* qo = q_out.has_value() ? q_out->data_ptr() : nullptr;
-    void* ks = seen[0].has_value() ? seen[0]->data_ptr() : nullptr;
-    void* vs = seen[1].has_value() ? seen[1]->data_ptr() : nullptr;
-    char* c = static_cast<char*>(kc.data_ptr());
+    const float k_scale = static_cast<float>(number(a[8])), v_scale = static_cast<float>(number(a[9]));
+    void* v_cache = ptr(a[7]);
     qsa_status_t rc;
-    if (format == 0) {
-      rc = qsa_kv_append(&s, qi, qo, k.data_ptr(), v.data_ptr(), table, positions, slots, c, ptr(a[7]), status, at.stream());
-    } else if (format == 1) {
-      rc = qsa_kv_append_fp8(&s, qi, qo, k.data_ptr(), v.data_ptr(), table, positions, slots,
-                             static_cast<float>(number(a[8])), static_cast<float>(number(a[9])), c, ptr(a[7]), ks, vs,
-                             status, at.stream());
-    } else {
-      s.bscale_stride_slot = s.kv_stride_slot;
-      s.bscale_stride_head = s.kv_stride_head;
-      rc = qsa_kv_append_fp4(&s, qi, qo, k.data_ptr(), v.data_ptr(), table, positions, slots,
-                             static_cast<float>(number(a[8])), static_cast<float>(number(a[9])), c, c + 256, c + 128,
-                             c + 272, ks, vs, status, at.stream());
+    {
+      const Unlocked threads;
+      if (q_in != nullptr) {
+        if (!q_out.has_value()) q_out = fresh(q_in->sizes(), at::kBFloat16, dev);
+        s.qo_stride_tok = q_out->stride(0);
+        s.qo_stride_head = q_out->stride(1);
+      }
+      for (auto& x : seen)
+        if (format != 0 && want && !x.has_value()) x = fresh(k.sizes(), at::kBFloat16, dev);
+      auto data = [](const std::optional<Tensor>& t) { return t.has_value() ? t->data_ptr() : nullptr; };
+      void *qi = q_in != nullptr ? q_in->data_ptr() : nullptr, *qo = data(q_out), *ks = data(seen[0]), *vs = data(seen[1]);
+      char* c = static_cast<char*>(kc.data_ptr());
+      if (format == 0) {
+        rc = qsa_kv_append(&s, qi, qo, k.data_ptr(), v.data_ptr(), table, positions, slots, c, v_cache, status,
+                           on.stream());
+      } else if (format == 1) {
+        rc = qsa_kv_append_fp8(&s, qi, qo, k.data_ptr(), v.data_ptr(), table, positions, slots, k_scale, v_scale, c,
+                               v_cache, ks, vs, status, on.stream());
+      } else {
+        s.bscale_stride_slot = s.kv_stride_slot;
+        s.bscale_stride_head = s.kv_stride_head;
+        rc = qsa_kv_append_fp4(&s, qi, qo, k.data_ptr(), v.data_ptr(), table, positions, slots, k_scale, v_scale, c,
+                               c + 256, c + 128, c + 272, ks, vs, status, on.stream());
+      }
     }
     return result(rc, q_out, seen[0], seen[1]);
   });
@@ -275,7 +294,7 @@ PyObject* sparse_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const bool decode = integer(a[0]) != 0;
     const Tensor& q = tensor(a[1], "q", at::kBFloat16, -1);
     const int dev = q.get_device();
-    const Launch at(a[15], dev);
+    const Launch on(a[15], dev);
     const Tensor& buf = tensor(a[2], "cache", at::kByte, dev);
     const Tensor& idx = tensor(a[3], "topk_idx", at::kInt, dev);
     need(q.dim() == 3 && idx.dim() == 3 && buf.dim() == 3, "q, the cache and topk_idx must be 3-d");
@@ -295,14 +314,13 @@ PyObject* sparse_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
       n_valid = static_cast<const int32_t*>(nv.data_ptr());
     }
     const int32_t* last = given(a[9]) ? per_token(a[9], "last_slot", s.num_tokens, dev) : nullptr;
-    Tensor out;
+    std::optional<Tensor> out;
     if (given(a[12])) {
       out = tensor(a[12], "out", at::kBFloat16, dev);
-      need(out.sizes() == q.sizes(), "out must be [T, Hq, D]");
-    } else {
-      out = fresh(q.sizes(), at::kBFloat16, dev);
+      need(out->sizes() == q.sizes(), "out must be [T, Hq, D]");
+      need(out->stride(2) == 1, kInner);
     }
-    need(q.stride(2) == 1 && out.stride(2) == 1 && buf.stride(2) == 1 && (s.topk <= 1 || idx.stride(2) == 1), kInner);
+    need(q.stride(2) == 1 && buf.stride(2) == 1 && (s.topk <= 1 || idx.stride(2) == 1), kInner);
     std::optional<Tensor> lse;
     s.lse_stride_tok = s.num_q_heads;
     const int want = PyObject_IsTrue(a[16]);
@@ -313,8 +331,6 @@ PyObject* sparse_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
                (s.num_q_heads <= 1 || lse->stride(1) == 1),
            "lse must be [T, Hq] with unit head stride");
       s.lse_stride_tok = lse->stride(0);
-    } else if (want) {
-      lse = fresh({s.num_tokens, s.num_q_heads}, at::kFloat, dev);
     }
     s.q_stride_tok = q.stride(0);
     s.q_stride_head = q.stride(1);
@@ -322,42 +338,47 @@ PyObject* sparse_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     s.kv_stride_head = buf.stride(1);
     s.idx_stride_tok = idx.stride(0);
     s.idx_stride_head = idx.stride(1);
-    s.o_stride_tok = out.stride(0);
-    s.o_stride_head = out.stride(1);
     int32_t* status = status_word(a[14], dev);
-    const char* c = static_cast<const char*>(buf.data_ptr());
-    const int32_t* list = static_cast<const int32_t*>(idx.data_ptr());
-    float* lp = lse.has_value() ? static_cast<float*>(lse->data_ptr()) : nullptr;
     const float ks = static_cast<float>(number(a[4])), vs = static_cast<float>(number(a[5])),
                 scale = static_cast<float>(number(a[7]));
+    const int32_t splits = decode ? integer32(a[10], "num_splits") : 0;
+    const int32_t block_size = decode ? 1 : integer32(a[8], "block_size");
+    Tensor ws;
+    size_t bytes = 0;
+    const bool own_ws = !decode || !given(a[11]);
+    if (!own_ws) {
+      if (!THPVariable_Check(a[11])) throw TypeFault("workspace must be a torch.Tensor");
+      ws = THPVariable_Unpack(a[11]);
+      need(ws.is_cuda() && ws.get_device() == dev && ws.is_contiguous(), "workspace must be a contiguous CUDA tensor");
+      bytes = ws.numel() * ws.element_size();
+    }
     qsa_status_t rc;
-    if (decode) {
-      const int32_t splits = integer32(a[10], "num_splits");
-      Tensor ws;
-      size_t bytes = 0;
-      if (given(a[11])) {
-        if (!THPVariable_Check(a[11])) throw TypeFault("workspace must be a torch.Tensor");
-        ws = THPVariable_Unpack(a[11]);
-        need(ws.is_cuda() && ws.get_device() == dev && ws.is_contiguous(), "workspace must be a contiguous CUDA tensor");
-        bytes = ws.numel() * ws.element_size();
-      }
+    {
+      const Unlocked threads;
+      if (!out.has_value()) out = fresh(q.sizes(), at::kBFloat16, dev);
+      if (want && !lse.has_value()) lse = fresh({s.num_tokens, s.num_q_heads}, at::kFloat, dev);
+      s.o_stride_tok = out->stride(0);
+      s.o_stride_head = out->stride(1);
+      const char* c = static_cast<const char*>(buf.data_ptr());
+      const int32_t* list = static_cast<const int32_t*>(idx.data_ptr());
+      float* lp = lse.has_value() ? static_cast<float*>(lse->data_ptr()) : nullptr;
       auto call = [&] {
+        if (!decode)
+          return qsa_sparse_prefill_fp4_fwd(&s, block_size, last, q.data_ptr(), c, c + 256, c + 128, c + 272,
+                                            buf.stride(0), buf.stride(1), list, n_valid, scale, ks, vs,
+                                            out->data_ptr(), lp, status, on.stream());
         return qsa_sparse_decode_fp4_fwd(&s, q.data_ptr(), c, c + 256, c + 128, c + 272, buf.stride(0), buf.stride(1),
-                                         list, n_valid, scale, ks, vs, out.data_ptr(), lp, status, splits,
-                                         ws.defined() ? ws.data_ptr() : nullptr, bytes, at.stream());
+                                         list, n_valid, scale, ks, vs, out->data_ptr(), lp, status, splits,
+                                         ws.defined() ? ws.data_ptr() : nullptr, bytes, on.stream());
       };
       rc = call();
       // refused for want of a workspace, where no cluster serves the call
-      if (rc == QSA_ERR_NULL && !given(a[11]) && (bytes = qsa_sparse_decode_fp4_workspace_bytes(&s, splits)) > 0) {
+      if (decode && rc == QSA_ERR_NULL && own_ws && (bytes = qsa_sparse_decode_fp4_workspace_bytes(&s, splits)) > 0) {
         ws = fresh({static_cast<int64_t>(bytes)}, at::kByte, dev);
         rc = call();
       }
-    } else {
-      rc = qsa_sparse_prefill_fp4_fwd(&s, integer32(a[8], "block_size"), last, q.data_ptr(), c, c + 256, c + 128,
-                                      c + 272, buf.stride(0), buf.stride(1), list, n_valid, scale, ks, vs,
-                                      out.data_ptr(), lp, status, at.stream());
     }
-    return result(rc, std::optional<Tensor>(out), lse);
+    return result(rc, out, lse);
   });
 }
 
