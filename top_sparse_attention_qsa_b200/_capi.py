@@ -18,6 +18,7 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libqsa.so")
+BINDING_PATH = os.path.join(_PKG, "_binding.so")
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(
@@ -26,7 +27,27 @@ if not os.path.exists(LIB_PATH):
 
 _lib = ctypes.CDLL(LIB_PATH)
 
-from . import _binding  # noqa: E402  (csrc/qsa_binding.cpp; links against libqsa.so)
+
+class _OnFirstUse:
+    """Stands for _binding (csrc/qsa_binding.cpp) until a call needs it: it is
+    compiled against one torch and one Python, and the calls that go through
+    ctypes alone do without it."""
+
+    def __getattr__(self, name):
+        global _binding
+        if not os.path.exists(BINDING_PATH):
+            raise ImportError(f"{BINDING_PATH} is missing: build it with `python -m top_sparse_attention_qsa_b200.build` "
+                              "(the cache appends and the 4-bit attention have no other path)")
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise ImportError(f"{BINDING_PATH} does not load; if torch or Python changed since it was built, build it "
+                              f"again with `python -m top_sparse_attention_qsa_b200.build` ({e})") from e
+        _binding = module
+        return getattr(module, name)
+
+
+_binding = _OnFirstUse()
 
 QSA_OK, QSA_ERR_NULL, QSA_ERR_SHAPE, QSA_ERR_UNSUPPORTED, QSA_ERR_ALIGN, QSA_ERR_CUDA, QSA_ERR_SCRATCH = range(7)
 NOALLOC_SCRATCH_BYTES = 16 << 20

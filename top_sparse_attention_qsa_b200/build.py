@@ -7,7 +7,7 @@
     _binding.so      the CPython binding of the calls whose marshalling counts
                      (csrc/qsa_binding.cpp; against torch and libqsa.so)
 
-    python -m top_sparse_attention_qsa_b200.build [--verbose]
+    python -m top_sparse_attention_qsa_b200.build [--verbose] [--no-binding]
 
 Both link the CUDA runtime statically and resolve the driver at run time, so
 they load on machines without a GPU (their entry points then return
@@ -101,14 +101,17 @@ def _build_binding(force: bool) -> None:
     os.replace(tmp, BINDING)
 
 
-def build(force: bool = False, verbose: bool = False, debug: bool = True) -> str:
-    """Builds libqsa.so, _binding.so and (debug=True) libqsa_debug.so; returns libqsa.so's path."""
+def build(force: bool = False, verbose: bool = False, debug: bool = True, binding: bool = True) -> str:
+    """Builds libqsa.so, (debug=True) libqsa_debug.so and (binding=True) _binding.so; returns libqsa.so's path.
+    The binding comes last: where it cannot be built (no torch, no Python headers), the error leaves the
+    libraries in place, and with them every call but the cache appends and the 4-bit attention."""
     _build_one(LIB, False, force, verbose)
-    _build_binding(force)
     if debug:
         _build_one(DEBUG_LIB, True, force, verbose)
+    if binding:
+        _build_binding(force)
     return LIB
 
 
 if __name__ == "__main__":
-    print(build(force=True, verbose="--verbose" in sys.argv))
+    print(build(force=True, verbose="--verbose" in sys.argv, binding="--no-binding" not in sys.argv))
