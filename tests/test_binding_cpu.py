@@ -67,3 +67,19 @@ def test_libraries_are_built_before_the_binding(monkeypatch):
         B.build()
     assert made == [B.LIB, B.DEBUG_LIB]
     assert B.build(binding=False) == B.LIB
+
+
+def test_a_binding_of_another_torch_is_built_again(monkeypatch, tmp_path):
+    """What the binding was compiled against decides beside the file times."""
+    B.build()
+    assert B.binding_up_to_date()
+    with open(B.BINDING_ABI) as f:
+        assert f.read() == B.binding_abi()
+    note = tmp_path / "abi"
+    monkeypatch.setattr(B, "BINDING_ABI", str(note))
+    assert not B.binding_up_to_date()                    # no note: built before there was one
+    note.write_text(B.binding_abi())
+    assert B.binding_up_to_date()
+    import torch
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    assert not B.binding_up_to_date()

@@ -27,6 +27,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libqsa.so")
 BINDING = os.path.join(PKG, "_binding.so")
+BINDING_ABI = BINDING + ".abi"
 DEBUG_LIB = os.path.join(PKG, "libqsa_debug.so")
 DEBUG_SOURCES = ("qsa_debug_api.cu",)
 
@@ -81,8 +82,22 @@ def _build_one(lib: str, debug: bool, force: bool, verbose: bool) -> str:
     return lib
 
 
+def binding_abi() -> str:
+    """The torch and the Python that a _binding.so built now belongs to (written beside it)."""
+    import torch
+    return (f"torch {torch.__version__}, cxx11 abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)}, "
+            f"{sysconfig.get_config_var('SOABI')}\n")
+
+
+def binding_up_to_date() -> bool:
+    if not up_to_date(BINDING) or os.path.getmtime(BINDING) < os.path.getmtime(LIB) or not os.path.exists(BINDING_ABI):
+        return False
+    with open(BINDING_ABI) as f:
+        return f.read() == binding_abi()
+
+
 def _build_binding(force: bool) -> None:
-    if not force and up_to_date(BINDING) and os.path.getmtime(BINDING) >= os.path.getmtime(LIB):
+    if not force and binding_up_to_date():
         return
     import torch
     base = os.path.dirname(torch.__file__)
@@ -98,7 +113,11 @@ def _build_binding(force: bool) -> None:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("g++ failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
+    if os.path.exists(BINDING_ABI):
+        os.remove(BINDING_ABI)                           # (it belongs to the binding that goes)
     os.replace(tmp, BINDING)
+    with open(BINDING_ABI, "w") as f:
+        f.write(binding_abi())
 
 
 def build(force: bool = False, verbose: bool = False, debug: bool = True, binding: bool = True) -> str:
