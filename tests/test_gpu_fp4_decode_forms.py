@@ -118,3 +118,21 @@ def test_nan_in_every_decode_form(C, form, heads):
     assert np.isnan(o[hit][:, 48:64]).all() and np.isfinite(np.delete(o[hit], np.s_[48:64], -1)).all()
     assert np.all(np.abs(R.f64(lse)[hit] - ref[1][hit]) <= ref[3][hit])
     clean_outside(out, lse)
+
+
+def test_rows_of_another_width_are_refused(C):
+    """A buffer put into an Fp4Cache past its constructor is checked by the calls."""
+    q, cache, ks, vs, g = case(C, 2, 64, (12, 1), seed=93)
+    idx = W.random_lists(2, 1, 8, 64, g, DEV)
+    k = torch.zeros((2, 1, 256), dtype=torch.bfloat16, device=DEV)
+    pos = torch.arange(2, dtype=torch.int32, device=DEV)
+    before = cache.buffer.clone()
+    whole = cache.buffer
+    cache.buffer = whole[..., :256]
+    for call in (lambda: C.sparse_prefill_fp4_fwd(q, cache, idx, ks, vs),
+                 lambda: C.sparse_decode_fp4_fwd(q, cache, idx, ks, vs),
+                 lambda: C.kv_append_fp4(k, k, pos, pos, None, cache, ks, vs)):
+        with pytest.raises(ValueError, match="288"):
+            call()
+    torch.cuda.synchronize()
+    assert torch.equal(whole, before)

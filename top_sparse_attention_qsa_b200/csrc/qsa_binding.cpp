@@ -298,6 +298,7 @@ PyObject* sparse_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor& buf = tensor(a[2], "cache", at::kByte, dev);
     const Tensor& idx = tensor(a[3], "topk_idx", at::kInt, dev);
     need(q.dim() == 3 && idx.dim() == 3 && buf.dim() == 3, "q, the cache and topk_idx must be 3-d");
+    need(buf.size(2) == 288, "the cache must be [S, Hkv, 288]");
     qsa_shape_t s = {};
     s.num_tokens = q.size(0);
     s.num_q_heads = size32(q.size(1));
