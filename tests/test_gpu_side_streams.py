@@ -152,3 +152,27 @@ def test_other_threads_run_while_a_launch_waits(C, call):
     assert waited >= 0.2, "the queue never filled"
     during = [t for t in ticks if a <= t <= b]
     assert len(during) > 0.1 * waited / 0.002, f"{len(during)} ticks in {waited:.2f} s"
+
+
+@pytest.mark.parametrize("heads", [(24, 2), (16, 2)])
+def test_two_decodes_through_workspaces_at_once(C, heads):
+    """Decodes whose chunks go through a workspace, on two streams at once, as when each runs alone."""
+    T, ctx, K, splits = 40, 700, 650, 3
+    runs = []
+    for seed in (97, 98):
+        q, cache, ks, vs, g = case(C, T, T * ctx, heads, seed)
+        idx = W.random_lists(T, 2, K, ctx, g, DEV) + (torch.arange(T, dtype=torch.int32, device=DEV) * ctx).view(T, 1, 1)
+        assert C.decode_fp4_workspace_bytes(q, cache, idx, splits) > 0
+        runs.append((q, cache, idx, ks, vs))
+    call = lambda r: C.sparse_decode_fp4_fwd(*r, num_splits=splits)  # noqa: E731
+    alone = [call(r) for r in runs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in runs]
+    outs = []
+    for _ in range(20):                                  # workspaces are let go and taken again with kernels in flight
+        for r, s in zip(runs, streams):
+            with torch.cuda.stream(s):
+                outs.append(call(r))
+    torch.cuda.synchronize()
+    for i, (o, l) in enumerate(outs):
+        assert torch.equal(o, alone[i % 2][0]) and torch.equal(l, alone[i % 2][1])
