@@ -520,8 +520,8 @@ qsa_status_t qsa_kv_append(const qsa_append_shape_t* shape, const void* q,
                            int32_t* status, void* stream);
 
 /*
- * Append to an FP8 E4M3 cache: byte = E4M3 value nearest to y / k_scale (V:
- * v_scale), ties to even, saturating at +-448; NaN stays NaN.  k_seen and
+ * Append to an FP8 E4M3 cache: byte = E4M3 value nearest to the FP32 quotient
+ * y / k_scale (V: v_scale), ties to even, saturating at +-448; NaN stays NaN.  k_seen and
  * v_seen (BF16 device [T, Hkv, 256] contiguous, or NULL) receive the values
  * as cached, stored value * scale, of every token whose position is valid
  * (padded ones included).  Scales must lie in [2^-100, 2^100]

@@ -32,8 +32,11 @@
 // us.  Four rows of any kind per warp, 8 dims per lane, took 49 and 61 us (565
 // warp instructions per four rows, three quarters of the lanes rotating dims
 // that do not turn), one row per warp 90 and 92.  Query rows per warp: 4 take
-// 42 us, 6 38, 12 (spills) 50; K and V rows: 1 take 41 us, 4 as long as 2, but
-// the 4-bit cache's 50 against 44.
+// 42 us, 6 38, 12 50; K and V rows: 1 take 41 us, 4 as long as 2, but the 4-bit
+// cache's 50 against 44.  64 registers spill 8, 12 and 48 bytes a lane (BF16,
+// E4M3, 4 bits).  The E4M3 cache (7810 tokens, (12,1), 118 MB) takes 21.9 us, 0.8
+// of them the divisions: products with a reciprocal would round otherwise next
+// to a border.
 #pragma once
 
 #include <cuda_bf16.h>

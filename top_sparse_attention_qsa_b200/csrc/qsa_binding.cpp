@@ -5,7 +5,7 @@
 // pointers, sizes and strides; every step of the computation runs in
 // libqsa.so's kernels.  These calls come once per layer and token, where a
 // kernel takes 3 to 10 us and the same checks in Python took 10 to 20: here
-// they take about one.
+// they take about one, and letting go of the interpreter's lock 0.1 to 0.4.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

@@ -44,12 +44,12 @@
 // The code rows sit in shared memory with 16-byte chunk c of row r at place
 // c ^ (r & 7): both read patterns and the copies are free of bank conflicts.
 //
-// What bounds it (that workload, per 128 keys of a list): 2170 cycles, in which
-// the MMA pipe is busy 1034, the ALU pipe (conversions, nibbles, addresses) 930
-// and half the issue slots are used by 4540 warp instructions.  The 128 output
-// accumulators leave two warps to a scheduler, too few to keep three pipes
-// busy at once; splitting a unit between warps cost more instructions than the
-// extra warps won.
+// What bounds it (that workload, per 128 keys of a list): 2150 cycles, in which
+// the MMA pipe is busy 1020, the ALU pipe (conversions, nibbles, addresses) 880
+// and half the issue slots are used by 4310 warp instructions.  The 128 output
+// accumulators (255 registers, 12 bytes of spills) leave two warps to a
+// scheduler, too few to keep three pipes busy at once; splitting a unit between
+// warps cost more instructions than the extra warps won.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -233,7 +233,7 @@ __device__ __forceinline__ void cluster_merge(uint32_t part, int chunks, int G, 
 // ------------------------------------------------------------------ units
 
 // The units of slot blockIdx.x + gridDim.x * (warp / W), then every gridDim.x *
-// (8 / W)-th after it, in decode_unit's order, carried in 32 bits from one to
+// (warps of a CTA / W)-th after it, in decode_unit's order, carried in 32 bits from one to
 // the next (the host refuses sizes that reach 2^31 a stride past the end).
 struct Walk {
   uint32_t per_head, rem, g, step, left;   // left: units still to do, this one included
